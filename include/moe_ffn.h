@@ -17,6 +17,15 @@
  * with library-owned scratch (moe_sort_static_ws) and a diagnostic of the
  * kernels' bounded waits (moe_selftest_bounded_wait).
  *
+ * For training the routed layer around expert products of the caller's own:
+ *
+ *   moe_permute        token rows sorted by expert
+ *   moe_unpermute      sorted rows back to token order, weights applied (with
+ *                      no weights it is the gradient of moe_permute)
+ *   moe_unpermute_bwd  its gradients: of the sorted rows and of the weights
+ *   moe_route_bwd      the gradient of the weights -> that of the logits
+ *   moe_grad_sumsq, moe_grad_clip   global gradient norm and clipping
+ *
  * Sources (page title, section):
  *  - dstair/gated-deltanet-nki-trainium, "FP8 MoE decode kernel
  *    (moe_fused_w8_35b)": the fused chain gate/up GEMM -> SwiGLU -> down GEMM
@@ -44,8 +53,8 @@
  *    back.  The first call of a process also does one-time host set-up (kernel
  *    attributes, driver entry points); make one call before capturing a CUDA
  *    graph, after which moe_route, moe_route_ex, moe_router, moe_sort,
- *    moe_expert_ffn, moe_expert_ffn_w8a8, moe_expert_ffn_combine and
- *    moe_combine may be captured.
+ *    moe_expert_ffn, moe_expert_ffn_w8a8, moe_expert_ffn_combine, moe_combine
+ *    and the training calls may be captured.
  *  - Return value: MOE_OK (0) or a negative moe_status.  On error nothing has
  *    been launched and moe_last_error() holds a message (thread-local, valid
  *    until the next call on the same thread).  MOE_ERR_CUDA reports a launch
@@ -480,6 +489,135 @@ MOE_API int moe_expert_ffn_combine(const uint16_t* x, int T, int H, int K, const
  * ------------------------------------------------------------------------- */
 MOE_API int moe_combine(const uint16_t* y_sorted, const int32_t* inv_route, const uint16_t* y_shared,
                 int T, int K, int H, void* out, int out_dtype, int32_t* status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows sorted by expert and back, for training.
+ *
+ * The steps around the sorted grouped GEMM -- the NKI library's Permute Routed
+ * Tokens and Top-K Reduce, the Nemotron-H page's unpermute-reduce
+ * (spark_model/layers/nemotron_moe.rs, `prefill` step 5) -- as calls of their
+ * own, in three row types and with their gradients, for callers whose expert
+ * products are not moe_expert_ffn's.  Common to the four forms:
+ *   dtype      MOE_DTYPE_BF16, MOE_DTYPE_F32 or MOE_DTYPE_F16: the type of
+ *              every row tensor of the call (each result row is rounded once
+ *              to it; sums are fp32).  Row tensors are [T, H] (token order) or
+ *              [T*K, H] (sorted order), 16-byte aligned, for any H >= 1
+ *   inv_route  [T, K] i32 as moe_sort writes it: the sorted position of route
+ *              t*K + j, or -1 for a route that was skipped.  Any other value
+ *              outside [0, T*K) is skipped like -1 (never read or written out
+ *              of bounds) and sets MOE_STATUS_BAD_MAP.  Positions are distinct
+ *              (moe_sort's are); a position given twice makes the rows of that
+ *              position those of either route
+ *   n_rows     optional device int32: the number of sorted rows in use, which
+ *              is expert_offsets[E] (pass expert_offsets + E).  The sorted
+ *              rows written by the call (x_sorted, dy_sorted) from n_rows on
+ *              are then set to zero; with NULL they are left as they were
+ *   status     optional device int32, as moe_combine
+ * Outputs must not overlap inputs (MOE_ERR_INVALID_ARG).  Results do not
+ * depend on the launch: every sum has a fixed order.
+ * Limits: 0 <= T <= MOE_MAX_T, 1 <= K <= MOE_MAX_K, 1 <= H <= MOE_ROWS_MAX_H.
+ * ------------------------------------------------------------------------- */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+#define MOE_DTYPE_F16 2
+#define MOE_ROWS_MAX_H 65536
+
+/* moe_permute: x_sorted[inv_route[t*K + j], :] = x[t, :] (a copy, bit for bit). */
+MOE_API int moe_permute(const void* x, const int32_t* inv_route, const int32_t* n_rows, int T, int K, int H,
+                        int dtype, void* x_sorted, int32_t* status, moe_stream_t stream);
+
+/* moe_unpermute:
+ *   out[t, :] = sum_{j=0..K-1} topk_w[t, j] * y_sorted[inv_route[t*K + j], :]  (+ y_shared[t, :])
+ * summed in fp32 in slot order (then y_shared), one rounding at the end.
+ *   topk_w    [T, K] f32, or NULL for weights of 1.  A weight of exactly 0
+ *             adds nothing, whatever its row holds (infinities and NaN too)
+ *   y_shared  [T, H] or NULL: rows added with weight 1 (the shared expert)
+ * With topk_w and y_shared NULL this is the gradient of moe_permute:
+ *   dx[t, :] = sum_j dx_sorted[inv_route[t*K + j], :]. */
+MOE_API int moe_unpermute(const void* y_sorted, const int32_t* inv_route, const float* topk_w, const void* y_shared,
+                          int T, int K, int H, int dtype, void* out, int32_t* status, moe_stream_t stream);
+
+/* moe_unpermute_bwd: the gradients of moe_unpermute (that of y_shared is dout itself):
+ *   dy_sorted[inv_route[t*K + j], :] = topk_w[t, j] * dout[t, :]   (+0 for a weight of exactly 0)
+ *   dtopk_w[t, j] = sum_h dout[t, h] * y_sorted[inv_route[t*K + j], h]  in fp32; 0 for skipped routes
+ *   dy_sorted [T*K, H] or NULL, dtopk_w [T, K] f32 or NULL (not both): a
+ *   gradient that is not wanted costs nothing; y_sorted may be NULL when
+ *   dtopk_w is. */
+MOE_API int moe_unpermute_bwd(const void* dout, const void* y_sorted, const int32_t* inv_route, const float* topk_w,
+                              const int32_t* n_rows, int T, int K, int H, int dtype, void* dy_sorted, float* dtopk_w,
+                              int32_t* status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * moe_route_bwd -- the gradient of moe_route / moe_route_ex / moe_router's
+ * routing: from dtopk_w to the logits, the choice of experts held fixed.
+ *
+ * With s_j the score of choice j (softmax or sigmoid of its logit), G_j =
+ * dtopk_w[t, j] (0 where zero_mask is nonzero, whatever it holds) and q_j =
+ * s_j / sum_j' s_j':
+ *   softmax, renormalised: dl_j = scaling * q_j * (G_j - sum_i G_i q_i)
+ *   softmax, not:          dl_e = scaling * p_e * ([e chosen] G_e - sum_i G_i p_i), every e
+ *   sigmoid, renormalised: dl_j = scaling * q_j * (1 - s_j) * (G_j - sum_i G_i q_i)
+ *   sigmoid, not:          dl_j = scaling * G_j * s_j * (1 - s_j)
+ * and 0 for experts that were not chosen.  The selection bias and the groups
+ * only choose: they have no gradient.
+ *   logits    [T, E] f32 (read), topk_ids [T, K] i32 as the routing call wrote
+ *             it.  An id outside [0, E) is a choice that does not exist: it
+ *             takes no part, and sets MOE_STATUS_BAD_ID; an id given twice
+ *             collects both gradients
+ *   dtopk_w   [T, K] f32 (read)
+ *   cfg       as moe_router: NULL = moe_route's
+ *   zero_mask as the routing call was given, or NULL
+ *   dlogits   [T, E] f32 (written, every element)
+ * Limits and errors as moe_route_ex.
+ * ------------------------------------------------------------------------- */
+MOE_API int moe_route_bwd(const float* logits, const int32_t* topk_ids, const float* dtopk_w, int T, int E, int K,
+                          const moe_route_config* cfg, const uint8_t* zero_mask, float* dlogits, int32_t* status,
+                          moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The global 2-norm of many gradient tensors, and clipping by it.
+ *
+ * No counterpart on the pages: a layer of E experts has 3 E + 1 gradients, and
+ * their norm is one number.  A tensor is data[0 .. numel) of one of the three
+ * types, aligned to its element; the types may be mixed.  `out` is where
+ * moe_grad_clip writes the clipped tensor: the same pointer as data (in place)
+ * or memory that overlaps no other tensor of the list.  The list itself is
+ * host memory, read during the call.
+ *   moe_grad_sumsq:  *sumsq = sum over all tensors of data[i]^2 (f64), and, where
+ *     norm is not NULL, *norm = sqrt(*sumsq) (f32).  Squares of 4 to 8
+ *     neighbouring values are added in fp32, or in fp64 where fp32 would
+ *     overflow or vanish, and everything above that in fp64, in a fixed order.
+ *     Ranks that hold different tensors add their sumsq values (an all-reduce)
+ *     before clipping.
+ *   moe_grad_clip:  out = data * min(1, max_norm / (norm + eps)), rounded once,
+ *     with norm = sqrt(*sumsq) for a sumsq from the caller (device memory), or
+ *     of these tensors when sumsq is NULL.  *norm (f32, may be NULL) receives
+ *     it.  As the formula says, a norm of infinity scales finite gradients to
+ *     0, and one of NaN makes every gradient NaN; look at *norm to skip such
+ *     a step.
+ *   refs, n    n >= 0 tensors; numel 0 is valid (data may then be NULL)
+ *   workspace  moe_grad_workspace_bytes(n) bytes, any contents (moe_grad_clip
+ *              with a sumsq needs none)
+ *   max_norm   finite, >= 0; eps finite, >= 0
+ * moe_grad_refs_check is a host-only check of a list (launches nothing): the
+ * same checks as the calls, and that no two tensors, and no two outputs,
+ * overlap -- the calls leave that one to the caller (an element in two tensors
+ * would be scaled once or twice).
+ * ------------------------------------------------------------------------- */
+typedef struct moe_tensor_ref {
+    const void* data;
+    void* out; /* moe_grad_clip only */
+    int64_t numel;
+    int32_t dtype; /* MOE_DTYPE_* */
+    int32_t reserved; /* 0 */
+} moe_tensor_ref;
+
+MOE_API int moe_grad_refs_check(const moe_tensor_ref* refs, int n);
+MOE_API size_t moe_grad_workspace_bytes(int n);
+MOE_API int moe_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, float* norm, void* workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
+MOE_API int moe_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps,
+                          float* norm, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -35,7 +35,8 @@ EXPORTED = ("moe_last_error", "moe_abi_version", "moe_route", "moe_route_ex", "m
             "moe_sort", "moe_selftest_bounded_wait", "moe_router_plan_check",
             "moe_sort_static_ws", "moe_ffn_resolve_mode", "moe_ffn_workspace_bytes", "moe_expert_ffn", "moe_combine",
             "moe_ffn_combine_workspace_bytes", "moe_expert_ffn_combine", "moe_ffn_w8a8_workspace_bytes",
-            "moe_expert_ffn_w8a8")
+            "moe_expert_ffn_w8a8", "moe_permute", "moe_unpermute", "moe_unpermute_bwd", "moe_route_bwd",
+            "moe_grad_refs_check", "moe_grad_workspace_bytes", "moe_grad_sumsq", "moe_grad_clip")
 
 
 class MoEError(RuntimeError):
@@ -53,6 +54,11 @@ class _Experts(ctypes.Structure):
 class _RouteConfig(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int), ("sel_bias", ctypes.c_void_p), ("n_group", ctypes.c_int),
                 ("topk_group", ctypes.c_int), ("renormalize", ctypes.c_int), ("scaling", ctypes.c_float)]
+
+
+class _TensorRef(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -103,6 +109,22 @@ def lib() -> ctypes.CDLL:
             L.moe_expert_ffn_w8a8.restype = I
             L.moe_combine.argtypes = [P, P, P, I, I, I, P, I, P, P]
             L.moe_combine.restype = I
+            L.moe_permute.argtypes = [P, P, P, I, I, I, I, P, P, P]
+            L.moe_permute.restype = I
+            L.moe_unpermute.argtypes = [P, P, P, P, I, I, I, I, P, P, P]
+            L.moe_unpermute.restype = I
+            L.moe_unpermute_bwd.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P]
+            L.moe_unpermute_bwd.restype = I
+            L.moe_route_bwd.argtypes = [P, P, P, I, I, I, ctypes.POINTER(_RouteConfig), P, P, P, P]
+            L.moe_route_bwd.restype = I
+            L.moe_grad_refs_check.argtypes = [P, I]
+            L.moe_grad_refs_check.restype = I
+            L.moe_grad_workspace_bytes.argtypes = [I]
+            L.moe_grad_workspace_bytes.restype = S
+            L.moe_grad_sumsq.argtypes = [P, I, P, P, P, S, P]
+            L.moe_grad_sumsq.restype = I
+            L.moe_grad_clip.argtypes = [P, I, P, ctypes.c_float, ctypes.c_float, P, P, S, P]
+            L.moe_grad_clip.restype = I
             _L = L
     return _L
 
@@ -368,6 +390,295 @@ def moe_combine(y_sorted: torch.Tensor, inv_route: torch.Tensor, y_shared: Optio
     _check(lib().moe_combine(_ptr(y_sorted), _ptr(inv_route), _ptr(y_shared), T, K, H, _ptr(out),
                              out_dtype, _ptr(status), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- training: rows sorted by expert and back
+
+MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16 = 0, 1, 2
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16}
+
+
+def _tensor(name: str, t: torch.Tensor, dtype, dev, shape=None, numel=None) -> int:
+    """The address of a contiguous tensor of this type and size on this device."""
+    if t.device != dev or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor on the device of the call's first tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
+    if (shape is not None and t.shape != shape) or (numel is not None and t.numel() != numel):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape or "%d elements" % numel))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _row_dtype(name: str, t: torch.Tensor) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError("%s must be bfloat16, float16 or float32, not %s" % (name, t.dtype))
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix of rows, not of shape %s" % (name, tuple(t.shape)))
+    return d
+
+
+class _Here:
+    """Runs a call's allocations and launch on the tensors' device and the given stream."""
+
+    __slots__ = ("guards", "dev", "stream")
+
+    def __init__(self, dev: torch.device, stream=None):
+        self.dev, self.stream, self.guards = dev, stream, ()
+
+    def __enter__(self) -> int:
+        if not self.dev.type == "cuda":
+            raise ValueError("tensors must be CUDA tensors")
+        if self.stream is None:
+            if self.dev.index != torch.cuda.current_device():
+                self.guards = (torch.cuda.device(self.dev),)
+                self.guards[0].__enter__()
+            return torch.cuda.current_stream().cuda_stream
+        if self.stream.device != self.dev:
+            raise ValueError("the stream belongs to %s, the tensors to %s" % (self.stream.device, self.dev))
+        self.guards = (torch.cuda.stream(self.stream),)
+        self.guards[0].__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        for g in self.guards:
+            g.__exit__(*exc)
+
+
+def _last(expert_offsets: Optional[torch.Tensor], dev) -> Optional[int]:
+    """The address of expert_offsets[E], the number of sorted rows in use."""
+    if expert_offsets is None:
+        return None
+    n = expert_offsets.numel()
+    if n < 1:
+        raise ValueError("expert_offsets must hold E + 1 values")
+    return _tensor("expert_offsets", expert_offsets, torch.int32, dev) + 4 * (n - 1)
+
+
+def _opt(name, t, dtype, dev, shape=None, numel=None):
+    return None if t is None else _tensor(name, t, dtype, dev, shape, numel)
+
+
+def moe_permute(x: torch.Tensor, inv_route: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None,
+                x_sorted: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Token rows sorted by expert: x [T, H] (bf16, f16 or f32) and moe_sort's
+    inv_route [T*K] -> x_sorted [T*K, H].  With moe_sort's expert_offsets the
+    rows behind the last sorted one (routes that were skipped) are zeros;
+    without it they are left as they were."""
+    dt, dev = _row_dtype("x", x), x.device
+    T, H = x.shape
+    R = inv_route.numel()
+    K = R // T if T else 1
+    if R != T * K:
+        raise ValueError("inv_route holds %d positions: not a multiple of %d tokens" % (R, T))
+    with _Here(dev, stream) as s:
+        if x_sorted is None:
+            x_sorted = torch.empty((R, H), dtype=x.dtype, device=dev)
+        _check(lib().moe_permute(_tensor("x", x, x.dtype, dev), _tensor("inv_route", inv_route, torch.int32, dev),
+                                 _last(expert_offsets, dev), T, K, H, dt,
+                                 _tensor("x_sorted", x_sorted, x.dtype, dev, (R, H)),
+                                 _opt("status", status, torch.int32, dev), s))
+    return x_sorted
+
+
+def moe_permute_bwd(dx_sorted: torch.Tensor, inv_route: torch.Tensor, T: int, dx: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of moe_permute: dx_sorted [T*K, H] -> dx [T, H], each
+    token's rows added in fp32 in slot order (moe_unpermute without weights)."""
+    return _unpermute(dx_sorted, inv_route, None, None, T, dx, status, stream)
+
+
+def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch.Tensor,
+                  y_shared: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Sorted rows back to token order with the route weights applied:
+    y_sorted [T*K, H] (bf16, f16 or f32), topk_w [T, K] f32 (and y_shared
+    [T, H]) -> out [T, H], summed in fp32.  (moe_combine takes rows that carry
+    their weight already.)"""
+    return _unpermute(y_sorted, inv_route, topk_w, y_shared, topk_w.shape[0], out, status, stream)
+
+
+def _unpermute(y_sorted, inv_route, topk_w, y_shared, T, out, status, stream):
+    dt, dev = _row_dtype("sorted rows", y_sorted), y_sorted.device
+    R, H = y_sorted.shape
+    K = R // T if T else 1
+    if R != T * K:
+        raise ValueError("%d sorted rows: not a multiple of %d tokens" % (R, T))
+    row = y_sorted.dtype
+    with _Here(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, H), dtype=row, device=dev)
+        _check(lib().moe_unpermute(_tensor("sorted rows", y_sorted, row, dev),
+                                   _tensor("inv_route", inv_route, torch.int32, dev, numel=R),
+                                   _opt("topk_w", topk_w, torch.float32, dev, numel=R),
+                                   _opt("y_shared", y_shared, row, dev, (T, H)), T, K, H, dt,
+                                   _tensor("out", out, row, dev, (T, H)), _opt("status", status, torch.int32, dev),
+                                   s))
+    return out
+
+
+def moe_unpermute_bwd(dout: torch.Tensor, y_sorted: Optional[torch.Tensor], inv_route: torch.Tensor,
+                      topk_w: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None, need_dy: bool = True,
+                      need_dw: bool = True, dy_sorted: Optional[torch.Tensor] = None,
+                      dtopk_w: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of moe_unpermute: dout [T, H] -> (dy_sorted [T*K, H],
+    dtopk_w [T, K] f32), None in the place of one that is not needed (y_sorted
+    may be None when need_dw is False).  Rows behind the last sorted one as in
+    moe_permute."""
+    dt, dev = _row_dtype("dout", dout), dout.device
+    T, H = dout.shape
+    if topk_w.dim() != 2 or topk_w.shape[0] != T:
+        raise ValueError("topk_w must be [%d, K], not %s" % (T, tuple(topk_w.shape)))
+    K = topk_w.shape[1]
+    R, row = T * K, dout.dtype
+    if not (need_dy or need_dw):
+        return None, None
+    if need_dw and y_sorted is None:
+        raise ValueError("the weights' gradient needs y_sorted")
+    with _Here(dev, stream) as s:
+        if not need_dy:
+            dy_sorted = None
+        elif dy_sorted is None:
+            dy_sorted = torch.empty((R, H), dtype=row, device=dev)
+        if not need_dw:
+            dtopk_w = None
+        elif dtopk_w is None:
+            dtopk_w = torch.empty((T, K), dtype=torch.float32, device=dev)
+        _check(lib().moe_unpermute_bwd(_tensor("dout", dout, row, dev),
+                                       _tensor("y_sorted", y_sorted, row, dev, (R, H)) if need_dw else None,
+                                       _tensor("inv_route", inv_route, torch.int32, dev, numel=R),
+                                       _tensor("topk_w", topk_w, torch.float32, dev), _last(expert_offsets, dev), T,
+                                       K, H, dt, _opt("dy_sorted", dy_sorted, row, dev, (R, H)),
+                                       _opt("dtopk_w", dtopk_w, torch.float32, dev, (T, K)),
+                                       _opt("status", status, torch.int32, dev), s))
+    return dy_sorted, dtopk_w
+
+
+def moe_route_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.Tensor,
+                  score: int = MOE_SCORE_SOFTMAX, sel_bias: Optional[torch.Tensor] = None, n_group: int = 1,
+                  topk_group: Optional[int] = None, renormalize: bool = True, scaling: float = 1.0,
+                  zero_mask: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of moe_route / moe_route_ex / moe_router's routing: dtopk_w
+    [T, K] f32 -> dlogits [T, E] f32, the choice topk_ids held fixed.  Takes the
+    routing call's keyword arguments; sel_bias and the groups only choose, so
+    they take no part."""
+    dev = logits.device
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, K]")
+    T, E = logits.shape
+    K = topk_ids.shape[1]
+    f32 = torch.float32
+    cfg = _RouteConfig(int(score), None, int(n_group), int(n_group if topk_group is None else topk_group),
+                       int(bool(renormalize)), float(scaling))
+    if zero_mask is not None and zero_mask.dtype == torch.bool:
+        zero_mask = zero_mask.view(torch.uint8)
+    with _Here(dev, stream) as s:
+        if dlogits is None:
+            dlogits = torch.empty((T, E), dtype=f32, device=dev)
+        _check(lib().moe_route_bwd(_tensor("logits", logits, f32, dev),
+                                   _tensor("topk_ids", topk_ids, torch.int32, dev, (T, K)),
+                                   _tensor("dtopk_w", dtopk_w, f32, dev, (T, K)), T, E, K, ctypes.byref(cfg),
+                                   _opt("zero_mask", zero_mask, torch.uint8, dev, (T, K)),
+                                   _tensor("dlogits", dlogits, f32, dev, (T, E)),
+                                   _opt("status", status, torch.int32, dev), s))
+    return dlogits
+
+
+# ---------------------------------------------------------------- training: gradient norm and clipping
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether the elements fill one stretch of memory, in any order of the dimensions."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+class TensorList:
+    """Gradient tensors as moe_grad_norm, moe_grad_sumsq and moe_grad_clip take
+    them: bf16, f16 or f32 (mixed as they come), on one device, each dense in
+    memory, no two overlapping.  out: where moe_grad_clip writes the clipped
+    tensors (same shapes, strides and types; None: in place).  Checked once,
+    when the list is made; it holds the tensors, so a list made of
+    gradients that a later step replaces has to be made again."""
+
+    def __init__(self, tensors, out=None, device=None):
+        self.tensors = list(tensors)
+        self.out = self.tensors if out is None else list(out)
+        if len(self.out) != len(self.tensors):
+            raise ValueError("%d tensors but %d outputs" % (len(self.tensors), len(self.out)))
+        n = len(self.tensors)
+        if n:
+            device = self.tensors[0].device
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.n = n
+        self.refs = (_TensorRef * max(n, 1))()
+        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
+            dt = _DTYPES.get(t.dtype)
+            if dt is None:
+                raise ValueError("tensor %d must be bfloat16, float16 or float32, not %s" % (i, t.dtype))
+            if not t.is_cuda or t.device != self.device or o.device != self.device:
+                raise ValueError("tensor %d: the tensors and outputs must be CUDA tensors on one device" % i)
+            if o is not t and (o.dtype != t.dtype or o.shape != t.shape or (t.numel() and o.stride() != t.stride())):
+                raise ValueError("output %d must have the shape, strides and type of its tensor" % i)
+            if not _dense(t):
+                raise ValueError("tensor %d must be dense in memory (strides %s)" % (i, t.stride()))
+            self.refs[i] = _TensorRef(t.data_ptr(), o.data_ptr(), t.numel(), dt, 0)
+        _check(lib().moe_grad_refs_check(self.refs, n))
+        self.workspace_bytes = int(lib().moe_grad_workspace_bytes(n))
+
+
+def _tensor_list(tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def moe_grad_sumsq(tensors, stream=None, norm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The sum of squares over all tensors, f64 [] on the device (what ranks that
+    hold different tensors add up before moe_grad_clip).  tensors: a
+    TensorList or a sequence of tensors.  norm: an f32 [] that receives the root."""
+    tl = _tensor_list(tensors)
+    with _Here(tl.device, stream) as s:
+        sumsq = torch.empty((), dtype=torch.float64, device=tl.device)
+        ws = torch.empty(tl.workspace_bytes, dtype=torch.uint8, device=tl.device)
+        _check(lib().moe_grad_sumsq(tl.refs, tl.n, sumsq.data_ptr(), _opt("norm", norm, torch.float32, tl.device, ()),
+                                    ws.data_ptr(), tl.workspace_bytes, s))
+    return sumsq
+
+
+def moe_grad_norm(tensors, stream=None) -> torch.Tensor:
+    """The 2-norm over all tensors as one vector, f32 [] on the device."""
+    tl = _tensor_list(tensors)
+    with _Here(tl.device, stream):
+        norm = torch.empty((), dtype=torch.float32, device=tl.device)
+    moe_grad_sumsq(tl, stream, norm)
+    return norm
+
+
+def moe_grad_clip(tensors, max_norm: float, eps: float = 1e-6, sumsq: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Scales the tensors by min(1, max_norm / (norm + eps)), in place or into
+    the list's outputs, and returns the norm before that, f32 [] on the device.
+    sumsq: the f64 [] sum of squares to take the norm from (over more tensors
+    than these, such as those of other ranks); None: of these tensors."""
+    tl = _tensor_list(tensors)
+    with _Here(tl.device, stream) as s:
+        norm = torch.empty((), dtype=torch.float32, device=tl.device)
+        ws = torch.empty(tl.workspace_bytes, dtype=torch.uint8, device=tl.device) if sumsq is None else None
+        _check(lib().moe_grad_clip(tl.refs, tl.n, _opt("sumsq", sumsq, torch.float64, tl.device, numel=1),
+                                   float(max_norm), float(eps), norm.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), tl.workspace_bytes if ws is not None else 0,
+                                   s))
+    return norm
 
 
 # ---------------------------------------------------------------- whole layer

@@ -7,7 +7,9 @@
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
+#include <stdlib.h>
 
+#include <algorithm>
 #include <mutex>
 #include <string>
 
@@ -641,6 +643,211 @@ int moe_combine(const uint16_t* y_sorted, const int32_t* inv_route, const uint16
     cudaError_t e = moe::launch_combine(y_sorted, inv_route, y_shared, T, K, H, out,
                                         out_dtype == MOE_OUT_F32, status, stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine launch");
+}
+
+namespace {
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
+// Sizes and type common to the row calls.
+int check_rows(const char* fn, int T, int K, int H, int dtype) {
+    if (T < 0 || T > MOE_MAX_T) return fail(MOE_ERR_INVALID_ARG, "%s: T=%d must be in 0..=%d", fn, T, MOE_MAX_T);
+    if (K < 1 || K > MOE_MAX_K) return fail(MOE_ERR_INVALID_ARG, "%s: K=%d must be in 1..=%d", fn, K, MOE_MAX_K);
+    if (H < 1 || H > MOE_ROWS_MAX_H)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: H=%d must be in 1..=%d", fn, H, MOE_ROWS_MAX_H);
+    if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_F16)
+        return fail(MOE_ERR_INVALID_ARG, "%s: dtype=%d is not BF16/F32/F16", fn, dtype);
+    return MOE_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+int moe_permute(const void* x, const int32_t* inv_route, const int32_t* n_rows, int T, int K, int H, int dtype,
+                void* x_sorted, int32_t* status, moe_stream_t stream) {
+    g_err.clear();
+    if (int rc = check_rows("moe_permute", T, K, H, dtype)) return rc;
+    if (T == 0) return MOE_OK;
+    if (!x || !inv_route || !x_sorted)
+        return fail(MOE_ERR_INVALID_ARG, "moe_permute: x, inv_route and x_sorted must not be NULL");
+    if (!aligned16(x) || !aligned16(inv_route) || !aligned16(x_sorted) || !aligned4(n_rows) || !aligned4(status))
+        return fail(MOE_ERR_MISALIGNED,
+                    "moe_permute: tensor bases must be 16-byte aligned, n_rows and status 4-byte aligned");
+    const size_t row = static_cast<size_t>(H) * moe::dtype_bytes(dtype), R = static_cast<size_t>(T) * K;
+    if (overlaps(x, T * row, x_sorted, R * row) || overlaps(inv_route, R * 4, x_sorted, R * row))
+        return fail(MOE_ERR_INVALID_ARG, "moe_permute: x_sorted overlaps an input");
+    const moe::RowsArgs a{inv_route, n_rows, T, K, H, dtype, status};
+    cudaError_t e = moe::launch_permute(a, x, x_sorted, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_permute launch");
+}
+
+int moe_unpermute(const void* y_sorted, const int32_t* inv_route, const float* topk_w, const void* y_shared, int T,
+                  int K, int H, int dtype, void* out, int32_t* status, moe_stream_t stream) {
+    g_err.clear();
+    if (int rc = check_rows("moe_unpermute", T, K, H, dtype)) return rc;
+    if (T == 0) return MOE_OK;
+    if (!y_sorted || !inv_route || !out)
+        return fail(MOE_ERR_INVALID_ARG, "moe_unpermute: y_sorted, inv_route and out must not be NULL");
+    if (!aligned16(y_sorted) || !aligned16(inv_route) || !aligned16(topk_w) || !aligned16(y_shared) ||
+        !aligned16(out) || !aligned4(status))
+        return fail(MOE_ERR_MISALIGNED,
+                    "moe_unpermute: tensor bases must be 16-byte aligned and status 4-byte aligned");
+    const size_t row = static_cast<size_t>(H) * moe::dtype_bytes(dtype), R = static_cast<size_t>(T) * K;
+    if (overlaps(y_sorted, R * row, out, T * row) || overlaps(y_shared, T * row, out, T * row) ||
+        overlaps(inv_route, R * 4, out, T * row) || overlaps(topk_w, R * 4, out, T * row))
+        return fail(MOE_ERR_INVALID_ARG, "moe_unpermute: out overlaps an input");
+    const moe::RowsArgs a{inv_route, nullptr, T, K, H, dtype, status};
+    cudaError_t e = moe::launch_unpermute(a, y_sorted, topk_w, y_shared, out, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_unpermute launch");
+}
+
+int moe_unpermute_bwd(const void* dout, const void* y_sorted, const int32_t* inv_route, const float* topk_w,
+                      const int32_t* n_rows, int T, int K, int H, int dtype, void* dy_sorted, float* dtopk_w,
+                      int32_t* status, moe_stream_t stream) {
+    g_err.clear();
+    if (int rc = check_rows("moe_unpermute_bwd", T, K, H, dtype)) return rc;
+    if (T == 0) return MOE_OK;
+    if (!dout || !inv_route || (!dy_sorted && !dtopk_w))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "moe_unpermute_bwd: dout, inv_route and one of dy_sorted and dtopk_w must not be NULL");
+    if (dtopk_w && !y_sorted) return fail(MOE_ERR_INVALID_ARG, "moe_unpermute_bwd: dtopk_w needs y_sorted");
+    if (!aligned16(dout) || !aligned16(y_sorted) || !aligned16(inv_route) || !aligned16(topk_w) ||
+        !aligned16(dy_sorted) || !aligned16(dtopk_w) || !aligned4(n_rows) || !aligned4(status))
+        return fail(MOE_ERR_MISALIGNED,
+                    "moe_unpermute_bwd: tensor bases must be 16-byte aligned, n_rows and status 4-byte aligned");
+    const size_t row = static_cast<size_t>(H) * moe::dtype_bytes(dtype), R = static_cast<size_t>(T) * K;
+    const struct { const void* p; size_t n; } in[] = {{dout, T * row}, {dtopk_w ? y_sorted : nullptr, R * row},
+                                                      {inv_route, R * 4}, {topk_w, R * 4}};
+    for (const auto& i : in)
+        if (overlaps(i.p, i.n, dy_sorted, R * row) || overlaps(i.p, i.n, dtopk_w, R * 4))
+            return fail(MOE_ERR_INVALID_ARG, "moe_unpermute_bwd: an output overlaps an input");
+    if (overlaps(dy_sorted, R * row, dtopk_w, R * 4))
+        return fail(MOE_ERR_INVALID_ARG, "moe_unpermute_bwd: the outputs overlap");
+    const moe::RowsArgs a{inv_route, n_rows, T, K, H, dtype, status};
+    cudaError_t e = moe::launch_unpermute_bwd(a, dout, y_sorted, topk_w, dy_sorted, dtopk_w, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_unpermute_bwd launch");
+}
+
+int moe_route_bwd(const float* logits, const int32_t* topk_ids, const float* dtopk_w, int T, int E, int K,
+                  const moe_route_config* cfg, const uint8_t* zero_mask, float* dlogits, int32_t* status,
+                  moe_stream_t stream) {
+    g_err.clear();
+    int rc = check_topk(T, E, K);
+    if (rc) return rc;
+    if (cfg) {
+        rc = check_route_cfg("moe_route_bwd", cfg, E, K);
+        if (rc && rc != MOE_ERR_MISALIGNED) return rc;  // the bias takes no part here
+    }
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !dtopk_w || !dlogits)
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_bwd: logits, topk_ids, dtopk_w and dlogits must not be NULL");
+    if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(dtopk_w) || !aligned16(dlogits) || !aligned4(status))
+        return fail(MOE_ERR_MISALIGNED, "moe_route_bwd: tensor bases must be 16-byte aligned and status 4-byte aligned");
+    const size_t out = static_cast<size_t>(T) * E * 4, R = static_cast<size_t>(T) * K;
+    if (overlaps(logits, out, dlogits, out) || overlaps(topk_ids, R * 4, dlogits, out) ||
+        overlaps(dtopk_w, R * 4, dlogits, out) || overlaps(zero_mask, R, dlogits, out))
+        return fail(MOE_ERR_INVALID_ARG, "moe_route_bwd: dlogits overlaps an input");
+    g_err.clear();
+    const moe::RouteCfg rc_dev = cfg ? moe::RouteCfg{cfg->score, nullptr, 1, 1, cfg->renormalize, cfg->scaling}
+                                     : moe::RouteCfg{MOE_SCORE_SOFTMAX, nullptr, 1, 1, 1, 1.f};
+    cudaError_t e = moe::launch_route_bwd(logits, topk_ids, dtopk_w, T, E, K, rc_dev, zero_mask, dlogits, status,
+                                          stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_bwd launch");
+}
+
+namespace {
+
+int check_refs(const char* fn, const moe_tensor_ref* refs, int n, bool outs) {
+    if (n < 0 || (n > 0 && !refs)) return fail(MOE_ERR_INVALID_ARG, "%s: n=%d tensors, refs %p", fn, n, (const void*)refs);
+    for (int i = 0; i < n; ++i) {
+        const moe_tensor_ref& r = refs[i];
+        if (r.dtype != MOE_DTYPE_BF16 && r.dtype != MOE_DTYPE_F32 && r.dtype != MOE_DTYPE_F16)
+            return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: dtype=%d is not BF16/F32/F16", fn, i, r.dtype);
+        if (r.numel < 0 || r.numel > (int64_t(1) << 44) || r.reserved != 0)
+            return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: numel=%lld or its reserved field is out of range", fn, i,
+                        static_cast<long long>(r.numel));
+        if (r.numel == 0) continue;
+        if (!r.data || (outs && !r.out)) return fail(MOE_ERR_INVALID_ARG, "%s: tensor %d: NULL pointer", fn, i);
+        const uintptr_t odd = moe::dtype_bytes(r.dtype) - 1;
+        if ((reinterpret_cast<uintptr_t>(r.data) & odd) || (outs && (reinterpret_cast<uintptr_t>(r.out) & odd)))
+            return fail(MOE_ERR_MISALIGNED, "%s: tensor %d is not aligned to its elements", fn, i);
+    }
+    if (!moe::grad_chunks_fit(refs, n))
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: the tensors hold more values than one call takes", fn);
+    return MOE_OK;
+}
+
+int check_grad_workspace(const char* fn, int n, const void* workspace, size_t workspace_bytes) {
+    const size_t need = moe::grad_workspace_bytes(n);
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
+    if (!aligned16(workspace)) return fail(MOE_ERR_MISALIGNED, "%s: the workspace must be 16-byte aligned", fn);
+    return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_grad_workspace_bytes(int n) { return n < 1 ? 0 : moe::grad_workspace_bytes(n); }
+
+int moe_grad_refs_check(const moe_tensor_ref* refs, int n) {
+    g_err.clear();
+    const char* fn = "moe_grad_refs_check";
+    if (int rc = check_refs(fn, refs, n, false)) return rc;
+    struct Span {
+        uintptr_t begin, end;
+        int tensor, data, out;  // the span's tensor, and whether it is its data, its output or both
+    };
+    Span* s = static_cast<Span*>(malloc(sizeof(Span) * (2 * static_cast<size_t>(n) + 1)));
+    if (!s) return fail(MOE_ERR_INVALID_ARG, "%s: out of host memory for %d tensors", fn, n);
+    size_t m = 0;
+    for (int i = 0; i < n; ++i) {
+        const moe_tensor_ref& r = refs[i];
+        if (r.numel == 0) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(r.numel) * moe::dtype_bytes(r.dtype);
+        const uintptr_t d = reinterpret_cast<uintptr_t>(r.data), o = reinterpret_cast<uintptr_t>(r.out);
+        s[m++] = {d, d + bytes, i, 1, o == d};
+        if (r.out && o != d) s[m++] = {o, o + bytes, i, 0, 1};
+    }
+    std::sort(s, s + m, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    int rc = MOE_OK;
+    for (size_t i = 1; i < m && !rc; ++i) {
+        // Spans before i end at or before s[i - 1].end as long as none overlapped.
+        if (s[i].begin < s[i - 1].end)
+            rc = fail(MOE_ERR_INVALID_ARG, "%s: tensor %d%s overlaps tensor %d%s", fn, s[i - 1].tensor,
+                      s[i - 1].data ? "" : "'s output", s[i].tensor, s[i].data ? "" : "'s output");
+    }
+    free(s);
+    return rc;
+}
+
+int moe_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, float* norm, void* workspace,
+                   size_t workspace_bytes, moe_stream_t stream) {
+    g_err.clear();
+    if (int rc = check_refs("moe_grad_sumsq", refs, n, false)) return rc;
+    if (!sumsq) return fail(MOE_ERR_INVALID_ARG, "moe_grad_sumsq: sumsq must not be NULL");
+    if ((reinterpret_cast<uintptr_t>(sumsq) & 7) || !aligned4(norm))
+        return fail(MOE_ERR_MISALIGNED, "moe_grad_sumsq: sumsq must be 8-byte aligned and norm 4-byte aligned");
+    if (int rc = check_grad_workspace("moe_grad_sumsq", n, workspace, workspace_bytes)) return rc;
+    cudaError_t e = moe::launch_grad_sumsq(refs, n, sumsq, norm, workspace, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grad_sumsq launch");
+}
+
+int moe_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps, float* norm,
+                  void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    g_err.clear();
+    if (int rc = check_refs("moe_grad_clip", refs, n, true)) return rc;
+    if (!isfinite(max_norm) || max_norm < 0.f || !isfinite(eps) || eps < 0.f)
+        return fail(MOE_ERR_INVALID_ARG, "moe_grad_clip: max_norm and eps must be finite and >= 0");
+    if ((reinterpret_cast<uintptr_t>(sumsq) & 7) || !aligned4(norm))
+        return fail(MOE_ERR_MISALIGNED, "moe_grad_clip: sumsq must be 8-byte aligned and norm 4-byte aligned");
+    if (!sumsq)
+        if (int rc = check_grad_workspace("moe_grad_clip", n, workspace, workspace_bytes)) return rc;
+    cudaError_t e = moe::launch_grad_clip(refs, n, sumsq, max_norm, eps, norm, workspace, stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grad_clip launch");
 }
 
 }  // extern "C"

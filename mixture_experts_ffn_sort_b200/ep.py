@@ -23,8 +23,9 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import (MOE_MODE_AUTO, MOE_MODE_DECODE, MOE_OUT_BF16, MOE_OUT_F32, Experts, moe_combine, moe_expert_ffn,
-               moe_ffn_workspace_bytes, moe_route, moe_sort, moe_sort_workspace_bytes)
+from . import (MOE_MODE_AUTO, MOE_MODE_DECODE, MOE_OUT_BF16, MOE_OUT_F32, Experts, TensorList, moe_combine,
+               moe_expert_ffn, moe_ffn_workspace_bytes, moe_grad_clip, moe_grad_sumsq, moe_route, moe_sort,
+               moe_sort_workspace_bytes)
 
 
 def expert_range(E: int, rank: int, world: int) -> Tuple[int, int]:
@@ -219,3 +220,20 @@ class ExpertParallelPrefill:
         return self.finish(y_back, x, out_dtype)
 
     __call__ = forward
+
+
+# ---------------------------------------------------------------- training: the norm of sharded gradients
+
+def clip_grad_norm(expert_grads, replicated_grads, max_norm: float, eps: float = 1e-6, group=None) -> torch.Tensor:
+    """Clip one rank's gradients in place by the norm over all ranks: the
+    expert gradients differ from rank to rank (their sums of squares are added
+    over the group), the replicated ones (router, shared expert, already
+    reduced) are the same on every rank and count once.  Returns the norm
+    before clipping, f32 [] on the device; no host synchronisation.  Every
+    rank calls it, with an empty list where it has none."""
+    own, shared = list(expert_grads), list(replicated_grads)
+    every = TensorList(own + shared)
+    total = reduce_partials(moe_grad_sumsq(own if own else TensorList([], device=every.device)), group)
+    if shared:
+        total = total + moe_grad_sumsq(shared)
+    return moe_grad_clip(every, max_norm, eps, sumsq=total)
