@@ -9,6 +9,7 @@ fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -398,17 +399,42 @@ MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16 = 0, 1, 2
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16}
 
 
-def _tensor(name: str, t: torch.Tensor, dtype, dev, shape=None, numel=None) -> int:
-    """The address of a contiguous tensor of this type and size on this device."""
-    if t.device != dev or not t.is_cuda:
+def _refuse(name: str, t: torch.Tensor, dtype, idx: int, shape):
+    if t.get_device() != idx or idx < 0:
         raise ValueError("%s must be a CUDA tensor on the device of the call's first tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if (shape is not None and t.shape != shape) or (numel is not None and t.numel() != numel):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape or "%d elements" % numel))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _adr(name: str, t: torch.Tensor, dtype, idx: int, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on device idx."""
+    if t.dtype is not dtype or t.get_device() != idx or idx < 0 or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, dtype, idx, shape)
     return t.data_ptr()
+
+
+def _adr_n(name: str, t: torch.Tensor, dtype, idx: int, n: int) -> int:
+    """The same of a tensor of n elements in any shape."""
+    if t.dtype is not dtype or t.get_device() != idx or idx < 0 or t.numel() != n or not t.is_contiguous():
+        if t.numel() != n:
+            raise ValueError("%s holds %d values, expected %d" % (name, t.numel(), n))
+        _refuse(name, t, dtype, idx, t.shape)
+    return t.data_ptr()
+
+
+def _status_adr(status, idx: int) -> Optional[int]:
+    return None if status is None else _adr_n("status", status, torch.int32, idx, status.numel() or 1)
+
+
+def _in_use(expert_offsets: Optional[torch.Tensor], idx: int) -> Optional[int]:
+    """The address of expert_offsets[E], the number of sorted rows in use."""
+    if expert_offsets is None:
+        return None
+    n = expert_offsets.numel()
+    return _adr_n("expert_offsets", expert_offsets, torch.int32, idx, n or 1) + 4 * (n - 1)
 
 
 def _row_dtype(name: str, t: torch.Tensor) -> int:
@@ -420,45 +446,24 @@ def _row_dtype(name: str, t: torch.Tensor) -> int:
     return d
 
 
-class _Here:
-    """Runs a call's allocations and launch on the tensors' device and the given stream."""
-
-    __slots__ = ("guards", "dev", "stream")
-
-    def __init__(self, dev: torch.device, stream=None):
-        self.dev, self.stream, self.guards = dev, stream, ()
-
-    def __enter__(self) -> int:
-        if not self.dev.type == "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        if self.stream is None:
-            if self.dev.index != torch.cuda.current_device():
-                self.guards = (torch.cuda.device(self.dev),)
-                self.guards[0].__enter__()
-            return torch.cuda.current_stream().cuda_stream
-        if self.stream.device != self.dev:
-            raise ValueError("the stream belongs to %s, the tensors to %s" % (self.stream.device, self.dev))
-        self.guards = (torch.cuda.stream(self.stream),)
-        self.guards[0].__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        for g in self.guards:
-            g.__exit__(*exc)
+def _raw_stream(idx: int, stream) -> Optional[int]:
+    """The current stream's handle when a call for tensors of device idx can run
+    right here; None when the device or the stream has to be switched first."""
+    if idx < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is None and torch.cuda.current_device() == idx:
+        return torch._C._cuda_getCurrentRawStream(idx)
+    return None
 
 
-def _last(expert_offsets: Optional[torch.Tensor], dev) -> Optional[int]:
-    """The address of expert_offsets[E], the number of sorted rows in use."""
-    if expert_offsets is None:
-        return None
-    n = expert_offsets.numel()
-    if n < 1:
-        raise ValueError("expert_offsets must hold E + 1 values")
-    return _tensor("expert_offsets", expert_offsets, torch.int32, dev) + 4 * (n - 1)
-
-
-def _opt(name, t, dtype, dev, shape=None, numel=None):
-    return None if t is None else _tensor(name, t, dtype, dev, shape, numel)
+def _there(idx: int, stream):
+    """A context in which device idx, and the given stream, are the current ones: the call's
+    launches and its allocations belong to them."""
+    if stream is None:
+        return torch.cuda.device(idx)
+    if stream.device.index != idx:
+        raise ValueError("the stream belongs to %s, the tensors to cuda:%d" % (stream.device, idx))
+    return torch.cuda.stream(stream)
 
 
 def moe_permute(x: torch.Tensor, inv_route: torch.Tensor, expert_offsets: Optional[torch.Tensor] = None,
@@ -468,19 +473,24 @@ def moe_permute(x: torch.Tensor, inv_route: torch.Tensor, expert_offsets: Option
     inv_route [T*K] -> x_sorted [T*K, H].  With moe_sort's expert_offsets the
     rows behind the last sorted one (routes that were skipped) are zeros;
     without it they are left as they were."""
-    dt, dev = _row_dtype("x", x), x.device
+    idx = x.get_device()
+    s = _raw_stream(idx, stream)
+    if s is None:
+        with _there(idx, stream):
+            return moe_permute(x, inv_route, expert_offsets, x_sorted, status)
+    dt, row = _row_dtype("x", x), x.dtype
     T, H = x.shape
     R = inv_route.numel()
     K = R // T if T else 1
     if R != T * K:
         raise ValueError("inv_route holds %d positions: not a multiple of %d tokens" % (R, T))
-    with _Here(dev, stream) as s:
-        if x_sorted is None:
-            x_sorted = torch.empty((R, H), dtype=x.dtype, device=dev)
-        _check(lib().moe_permute(_tensor("x", x, x.dtype, dev), _tensor("inv_route", inv_route, torch.int32, dev),
-                                 _last(expert_offsets, dev), T, K, H, dt,
-                                 _tensor("x_sorted", x_sorted, x.dtype, dev, (R, H)),
-                                 _opt("status", status, torch.int32, dev), s))
+    if x_sorted is None:
+        x_sorted = x.new_empty((R, H))
+        out = x_sorted.data_ptr()
+    else:
+        out = _adr("x_sorted", x_sorted, row, idx, (R, H))
+    _check((_L or lib()).moe_permute(_adr_n("x", x, row, idx, T * H), _adr_n("inv_route", inv_route, torch.int32, idx, R),
+                                     _in_use(expert_offsets, idx), T, K, H, dt, out, _status_adr(status, idx), s))
     return x_sorted
 
 
@@ -502,21 +512,26 @@ def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch
 
 
 def _unpermute(y_sorted, inv_route, topk_w, y_shared, T, out, status, stream):
-    dt, dev = _row_dtype("sorted rows", y_sorted), y_sorted.device
+    idx = y_sorted.get_device()
+    s = _raw_stream(idx, stream)
+    if s is None:
+        with _there(idx, stream):
+            return _unpermute(y_sorted, inv_route, topk_w, y_shared, T, out, status, None)
+    dt, row = _row_dtype("sorted rows", y_sorted), y_sorted.dtype
     R, H = y_sorted.shape
     K = R // T if T else 1
     if R != T * K:
         raise ValueError("%d sorted rows: not a multiple of %d tokens" % (R, T))
-    row = y_sorted.dtype
-    with _Here(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, H), dtype=row, device=dev)
-        _check(lib().moe_unpermute(_tensor("sorted rows", y_sorted, row, dev),
-                                   _tensor("inv_route", inv_route, torch.int32, dev, numel=R),
-                                   _opt("topk_w", topk_w, torch.float32, dev, numel=R),
-                                   _opt("y_shared", y_shared, row, dev, (T, H)), T, K, H, dt,
-                                   _tensor("out", out, row, dev, (T, H)), _opt("status", status, torch.int32, dev),
-                                   s))
+    if out is None:
+        out = y_sorted.new_empty((T, H))
+        to = out.data_ptr()
+    else:
+        to = _adr("out", out, row, idx, (T, H))
+    _check((_L or lib()).moe_unpermute(_adr_n("sorted rows", y_sorted, row, idx, R * H),
+                                       _adr_n("inv_route", inv_route, torch.int32, idx, R),
+                                       None if topk_w is None else _adr_n("topk_w", topk_w, torch.float32, idx, R),
+                                       None if y_shared is None else _adr("y_shared", y_shared, row, idx, (T, H)),
+                                       T, K, H, dt, to, _status_adr(status, idx), s))
     return out
 
 
@@ -528,33 +543,51 @@ def moe_unpermute_bwd(dout: torch.Tensor, y_sorted: Optional[torch.Tensor], inv_
     dtopk_w [T, K] f32), None in the place of one that is not needed (y_sorted
     may be None when need_dw is False).  Rows behind the last sorted one as in
     moe_permute."""
-    dt, dev = _row_dtype("dout", dout), dout.device
+    idx = dout.get_device()
+    s = _raw_stream(idx, stream)
+    if s is None:
+        with _there(idx, stream):
+            return moe_unpermute_bwd(dout, y_sorted, inv_route, topk_w, expert_offsets, need_dy, need_dw, dy_sorted,
+                                     dtopk_w, status)
+    dt, row = _row_dtype("dout", dout), dout.dtype
     T, H = dout.shape
     if topk_w.dim() != 2 or topk_w.shape[0] != T:
         raise ValueError("topk_w must be [%d, K], not %s" % (T, tuple(topk_w.shape)))
+    R = topk_w.numel()
     K = topk_w.shape[1]
-    R, row = T * K, dout.dtype
     if not (need_dy or need_dw):
         return None, None
-    if need_dw and y_sorted is None:
-        raise ValueError("the weights' gradient needs y_sorted")
-    with _Here(dev, stream) as s:
-        if not need_dy:
-            dy_sorted = None
-        elif dy_sorted is None:
-            dy_sorted = torch.empty((R, H), dtype=row, device=dev)
-        if not need_dw:
-            dtopk_w = None
-        elif dtopk_w is None:
-            dtopk_w = torch.empty((T, K), dtype=torch.float32, device=dev)
-        _check(lib().moe_unpermute_bwd(_tensor("dout", dout, row, dev),
-                                       _tensor("y_sorted", y_sorted, row, dev, (R, H)) if need_dw else None,
-                                       _tensor("inv_route", inv_route, torch.int32, dev, numel=R),
-                                       _tensor("topk_w", topk_w, torch.float32, dev), _last(expert_offsets, dev), T,
-                                       K, H, dt, _opt("dy_sorted", dy_sorted, row, dev, (R, H)),
-                                       _opt("dtopk_w", dtopk_w, torch.float32, dev, (T, K)),
-                                       _opt("status", status, torch.int32, dev), s))
+    dy = dw = y = None
+    if not need_dy:
+        dy_sorted = None
+    elif dy_sorted is None:
+        dy_sorted = dout.new_empty((R, H))
+        dy = dy_sorted.data_ptr()
+    else:
+        dy = _adr("dy_sorted", dy_sorted, row, idx, (R, H))
+    if not need_dw:
+        dtopk_w = None
+    else:
+        if y_sorted is None:
+            raise ValueError("the weights' gradient needs y_sorted")
+        y = _adr("y_sorted", y_sorted, row, idx, (R, H))
+        if dtopk_w is None:
+            dtopk_w = topk_w.new_empty((T, K))
+            dw = dtopk_w.data_ptr()
+        else:
+            dw = _adr("dtopk_w", dtopk_w, torch.float32, idx, (T, K))
+    _check((_L or lib()).moe_unpermute_bwd(_adr_n("dout", dout, row, idx, T * H), y,
+                                           _adr_n("inv_route", inv_route, torch.int32, idx, R),
+                                           _adr_n("topk_w", topk_w, torch.float32, idx, R),
+                                           _in_use(expert_offsets, idx), T, K, H, dt, dy, dw,
+                                           _status_adr(status, idx), s))
     return dy_sorted, dtopk_w
+
+
+@functools.lru_cache(maxsize=64)
+def _score_config(score: int, n_group: int, topk_group: int, renormalize: int, scaling: float):
+    """A routing configuration without a bias, read by the library only."""
+    return ctypes.pointer(_RouteConfig(score, None, n_group, topk_group, renormalize, scaling))
 
 
 def moe_route_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.Tensor,
@@ -566,25 +599,33 @@ def moe_route_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.T
     [T, K] f32 -> dlogits [T, E] f32, the choice topk_ids held fixed.  Takes the
     routing call's keyword arguments; sel_bias and the groups only choose, so
     they take no part."""
-    dev = logits.device
+    idx = logits.get_device()
+    s = _raw_stream(idx, stream)
+    if s is None:
+        with _there(idx, stream):
+            return moe_route_bwd(logits, topk_ids, dtopk_w, score, sel_bias, n_group, topk_group, renormalize,
+                                 scaling, zero_mask, dlogits, status)
     if logits.dim() != 2 or topk_ids.dim() != 2:
         raise ValueError("logits must be [T, E] and topk_ids [T, K]")
     T, E = logits.shape
     K = topk_ids.shape[1]
     f32 = torch.float32
-    cfg = _RouteConfig(int(score), None, int(n_group), int(n_group if topk_group is None else topk_group),
-                       int(bool(renormalize)), float(scaling))
-    if zero_mask is not None and zero_mask.dtype == torch.bool:
-        zero_mask = zero_mask.view(torch.uint8)
-    with _Here(dev, stream) as s:
-        if dlogits is None:
-            dlogits = torch.empty((T, E), dtype=f32, device=dev)
-        _check(lib().moe_route_bwd(_tensor("logits", logits, f32, dev),
-                                   _tensor("topk_ids", topk_ids, torch.int32, dev, (T, K)),
-                                   _tensor("dtopk_w", dtopk_w, f32, dev, (T, K)), T, E, K, ctypes.byref(cfg),
-                                   _opt("zero_mask", zero_mask, torch.uint8, dev, (T, K)),
-                                   _tensor("dlogits", dlogits, f32, dev, (T, E)),
-                                   _opt("status", status, torch.int32, dev), s))
+    mask = None
+    if zero_mask is not None:
+        if zero_mask.dtype is torch.bool:
+            zero_mask = zero_mask.view(torch.uint8)
+        mask = _adr("zero_mask", zero_mask, torch.uint8, idx, (T, K))
+    if dlogits is None:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        out = dlogits.data_ptr()
+    else:
+        out = _adr("dlogits", dlogits, f32, idx, (T, E))
+    cfg = _score_config(int(score), int(n_group), int(n_group if topk_group is None else topk_group),
+                        int(bool(renormalize)), float(scaling))
+    _check((_L or lib()).moe_route_bwd(_adr("logits", logits, f32, idx, (T, E)),
+                                       _adr("topk_ids", topk_ids, torch.int32, idx, (T, K)),
+                                       _adr("dtopk_w", dtopk_w, f32, idx, (T, K)), T, E, K, cfg, mask, out,
+                                       _status_adr(status, idx), s))
     return dlogits
 
 
@@ -618,10 +659,10 @@ class TensorList:
         n = len(self.tensors)
         if n:
             device = self.tensors[0].device
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        if self.device.type == "cuda" and self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
-        self.n = n
+        device = torch.device("cuda" if device is None else device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.n = device, n
         self.refs = (_TensorRef * max(n, 1))()
         for i, (t, o) in enumerate(zip(self.tensors, self.out)):
             dt = _DTYPES.get(t.dtype)
@@ -636,6 +677,10 @@ class TensorList:
             self.refs[i] = _TensorRef(t.data_ptr(), o.data_ptr(), t.numel(), dt, 0)
         _check(lib().moe_grad_refs_check(self.refs, n))
         self.workspace_bytes = int(lib().moe_grad_workspace_bytes(n))
+        # What the calls allocate their results and workspaces from (each call its own).
+        self.index = self.device.index
+        self.none32 = torch.empty(0, dtype=torch.float32, device=self.device)
+        self.none64 = torch.empty(0, dtype=torch.float64, device=self.device)
 
 
 def _tensor_list(tensors) -> TensorList:
@@ -647,20 +692,26 @@ def moe_grad_sumsq(tensors, stream=None, norm: Optional[torch.Tensor] = None) ->
     hold different tensors add up before moe_grad_clip).  tensors: a
     TensorList or a sequence of tensors.  norm: an f32 [] that receives the root."""
     tl = _tensor_list(tensors)
-    with _Here(tl.device, stream) as s:
-        sumsq = torch.empty((), dtype=torch.float64, device=tl.device)
-        ws = torch.empty(tl.workspace_bytes, dtype=torch.uint8, device=tl.device)
-        _check(lib().moe_grad_sumsq(tl.refs, tl.n, sumsq.data_ptr(), _opt("norm", norm, torch.float32, tl.device, ()),
-                                    ws.data_ptr(), tl.workspace_bytes, s))
+    s = _raw_stream(tl.index, stream)
+    if s is None:
+        with _there(tl.index, stream):
+            return moe_grad_sumsq(tl, None, norm)
+    sumsq = tl.none64.new_empty(())
+    ws = tl.none64.new_empty(tl.workspace_bytes // 8)
+    _check((_L or lib()).moe_grad_sumsq(tl.refs, tl.n, sumsq.data_ptr(),
+                                        None if norm is None else _adr("norm", norm, torch.float32, tl.index, ()),
+                                        ws.data_ptr(), tl.workspace_bytes, s))
     return sumsq
 
 
 def moe_grad_norm(tensors, stream=None) -> torch.Tensor:
     """The 2-norm over all tensors as one vector, f32 [] on the device."""
     tl = _tensor_list(tensors)
-    with _Here(tl.device, stream):
-        norm = torch.empty((), dtype=torch.float32, device=tl.device)
-    moe_grad_sumsq(tl, stream, norm)
+    if _raw_stream(tl.index, stream) is None:
+        with _there(tl.index, stream):
+            return moe_grad_norm(tl)
+    norm = tl.none32.new_empty(())
+    moe_grad_sumsq(tl, None, norm)
     return norm
 
 
@@ -671,13 +722,17 @@ def moe_grad_clip(tensors, max_norm: float, eps: float = 1e-6, sumsq: Optional[t
     sumsq: the f64 [] sum of squares to take the norm from (over more tensors
     than these, such as those of other ranks); None: of these tensors."""
     tl = _tensor_list(tensors)
-    with _Here(tl.device, stream) as s:
-        norm = torch.empty((), dtype=torch.float32, device=tl.device)
-        ws = torch.empty(tl.workspace_bytes, dtype=torch.uint8, device=tl.device) if sumsq is None else None
-        _check(lib().moe_grad_clip(tl.refs, tl.n, _opt("sumsq", sumsq, torch.float64, tl.device, numel=1),
-                                   float(max_norm), float(eps), norm.data_ptr(),
-                                   None if ws is None else ws.data_ptr(), tl.workspace_bytes if ws is not None else 0,
-                                   s))
+    s = _raw_stream(tl.index, stream)
+    if s is None:
+        with _there(tl.index, stream):
+            return moe_grad_clip(tl, max_norm, eps, sumsq)
+    norm = tl.none32.new_empty(())
+    if sumsq is None:
+        ws = tl.none64.new_empty(tl.workspace_bytes // 8)
+        given, work, size = None, ws.data_ptr(), tl.workspace_bytes
+    else:
+        given, work, size = _adr_n("sumsq", sumsq, torch.float64, tl.index, 1), None, 0
+    _check((_L or lib()).moe_grad_clip(tl.refs, tl.n, given, max_norm, eps, norm.data_ptr(), work, size, s))
     return norm
 
 
