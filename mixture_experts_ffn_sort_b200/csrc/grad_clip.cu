@@ -18,7 +18,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr long kChunk = static_cast<long>(kThreads) * 16 * kUnroll;  // bytes of a tensor per step of a block
-constexpr int kMaxBlocks = 148 * 8;
+constexpr int kPerSm = 6;
+constexpr int kMaxBlocks = 148 * kPerSm;
 
 template <int CAP>
 struct GradTable {
@@ -60,52 +61,77 @@ template <class E>
 __device__ __forceinline__ double vec_sumsq(const uint4& raw) {
     constexpr int N = 16 / sizeof(E);
     float f[N];
-    unpack<E, 16>(raw, f);
+    unpack<E>(raw, f);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
-    if (s > 1e-20f && s < 1e30f) return s;
+    if ((s > 1e-20f && s < 1e30f) || !(raw.x | raw.y | raw.z | raw.w)) return s;
     double d = 0.;
 #pragma unroll
     for (int i = 0; i < N; ++i) d = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), d);
     return d;
 }
 
-// Elements [begin, end) of a tensor that chunk k covers, as byte offsets from
-// the tensor's 16-byte boundary `base` (the element range starts at `skip`).
+// The bytes of a tensor that one step of a block covers: chunk k, as offsets
+// from the tensor's 16-byte boundary (its elements are [skip, end) of them).
+struct Span {
+    long lo, skip, end;
+    template <class E>
+    static __device__ __forceinline__ Span of(const void* src, long numel, long k) {
+        const long skip = static_cast<long>(reinterpret_cast<uintptr_t>(src) & 15);
+        return {k * kChunk, skip, skip + numel * static_cast<long>(sizeof(E))};
+    }
+    __device__ __forceinline__ bool inside() const { return lo >= skip && lo + kChunk <= end; }
+    __device__ __forceinline__ long at(int u) const {
+        return lo + (static_cast<long>(u) * kThreads + threadIdx.x) * 16;
+    }
+};
+
+// Calls f(byte offset) for this thread's element of the vectors that only in
+// part belong to the tensor: its first (before the first 16-byte boundary, or
+// all of a tensor within 16 bytes) and its last.  Lanes 0..7 take the elements
+// of the first, 32..39 those of the last.
+template <class E, class F>
+__device__ __forceinline__ void part_elements(const Span& s, F f) {
+    const int i = threadIdx.x & 31;
+    if (i >= kVec<E> || threadIdx.x >= 64) return;
+    const bool first = threadIdx.x < 32;
+    const long last = s.end & ~15L;  // start of the last vector, if it is not whole
+    const long o = first ? 0 : last;
+    if (o < s.lo || o >= s.lo + kChunk) return;
+    if (first ? s.skip == 0 && s.end >= 16 : last == s.end || last == 0) return;
+    const long b = o + i * static_cast<long>(sizeof(E));
+    if (b >= s.skip && b < s.end) f(b);
+}
+
 template <class E>
 __device__ __forceinline__ double chunk_sumsq(const void* src, long numel, long k) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(src);
-    const char* base = reinterpret_cast<const char*>(a & ~uintptr_t(15));
-    const long skip = static_cast<long>(a & 15), end = skip + numel * static_cast<long>(sizeof(E));
-    const long lo = k * kChunk;
+    const Span s = Span::of<E>(src, numel, k);
+    const char* base = static_cast<const char*>(src) - s.skip;
     double acc = 0.;
     uint4 v[kUnroll];
-    bool whole[kUnroll];
+    if (s.inside()) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const long o = lo + (static_cast<long>(u) * kThreads + threadIdx.x) * 16;
-        whole[u] = o >= skip && o + 16 <= end;
-        if (whole[u]) v[u] = __ldg(reinterpret_cast<const uint4*>(base + o));
-    }
+        for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(reinterpret_cast<const uint4*>(base + s.at(u)));
+    } else {  // the tensor's first or last chunk
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        if (whole[u]) {
-            acc += vec_sumsq<E>(v[u]);
-        } else {  // the first or last vector of the tensor, or beyond it
-            const long o = lo + (static_cast<long>(u) * kThreads + threadIdx.x) * 16;
-            for (long b = o; b < o + 16; b += sizeof(E))
-                if (b >= skip && b < end) {
-                    const double f = elem_to_float(*reinterpret_cast<const E*>(base + b));
-                    acc = fma(f, f, acc);
-                }
+        for (int u = 0; u < kUnroll; ++u) {
+            const long o = s.at(u);
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (o >= s.skip && o + 16 <= s.end) v[u] = __ldg(reinterpret_cast<const uint4*>(base + o));
         }
+        part_elements<E>(s, [&](long b) {
+            const double f = elem_to_float(*reinterpret_cast<const E*>(base + b));
+            acc = f * f;
+        });
     }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) acc += vec_sumsq<E>(v[u]);
     return acc;
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__ GradTable<CAP> tab,
+__global__ void __launch_bounds__(kThreads, kPerSm) sumsq_kernel(const __grid_constant__ GradTable<CAP> tab,
                                                          double* __restrict__ partial) {
     __shared__ double sh[kThreads / 32];
     double acc = 0.;
@@ -140,53 +166,61 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
 }
 
 template <class E>
+__device__ __forceinline__ uint4 scaled(const uint4& v, float f) {
+    float g[kVec<E>];
+    unpack<E>(v, g);
+#pragma unroll
+    for (int i = 0; i < kVec<E>; ++i) g[i] *= f;
+    return pack<E>(g);
+}
+
+template <class E>
 __device__ __forceinline__ void chunk_scale(const void* src, void* dst, long numel, long k, float f) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(src), d = reinterpret_cast<uintptr_t>(dst);
-    const long skip = static_cast<long>(a & 15), end = skip + numel * static_cast<long>(sizeof(E));
-    const char* base = reinterpret_cast<const char*>(a - skip);
-    char* to = reinterpret_cast<char*>(d - skip);  // 16-byte aligned when src and dst share their offset
-    const bool together = ((a ^ d) & 15) == 0;
-    const long lo = k * kChunk;
-    uint4 v[kUnroll];
-    bool whole[kUnroll];
+    const Span s = Span::of<E>(src, numel, k);
+    const char* base = static_cast<const char*>(src) - s.skip;
+    char* to = static_cast<char*>(dst) - s.skip;
+    const bool together = (reinterpret_cast<uintptr_t>(to) & 15) == 0;  // src and dst share their offset
+    if (together) {
+        uint4 v[kUnroll];
+        const bool inside = s.inside();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const long o = lo + (static_cast<long>(u) * kThreads + threadIdx.x) * 16;
-        whole[u] = together && o >= skip && o + 16 <= end;
-        if (whole[u]) v[u] = *reinterpret_cast<const uint4*>(base + o);
+        for (int u = 0; u < kUnroll; ++u)
+            if (inside || (s.at(u) >= s.skip && s.at(u) + 16 <= s.end))
+                v[u] = *reinterpret_cast<const uint4*>(base + s.at(u));
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (inside || (s.at(u) >= s.skip && s.at(u) + 16 <= s.end))
+                *reinterpret_cast<uint4*>(to + s.at(u)) = scaled<E>(v[u], f);
+        if (!inside)
+            part_elements<E>(s, [&](long b) {
+                *reinterpret_cast<E*>(to + b) =
+                    elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
+            });
+        return;
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const long o = lo + (static_cast<long>(u) * kThreads + threadIdx.x) * 16;
-        if (whole[u]) {
-            float g[16 / sizeof(E)];
-            unpack<E, 16>(v[u], g);
-#pragma unroll
-            for (int i = 0; i < static_cast<int>(16 / sizeof(E)); ++i) g[i] *= f;
-            *reinterpret_cast<uint4*>(to + o) = pack<E, 16>(g);
-        } else {
-            for (long b = o; b < o + 16; b += sizeof(E))
-                if (b >= skip && b < end) {
-                    const float g[1] = {elem_to_float(*reinterpret_cast<const E*>(base + b)) * f};
-                    *reinterpret_cast<raw_t<sizeof(E)>*>(to + b) = pack<E, sizeof(E)>(g);
-                }
-        }
-    }
+    // Another offset: element by element, neighbouring threads on neighbouring elements.
+    const long first = s.lo > s.skip ? s.lo : s.skip, past = s.lo + kChunk < s.end ? s.lo + kChunk : s.end;
+#pragma unroll 8
+    for (long b = first + threadIdx.x * static_cast<long>(sizeof(E)); b < past; b += kThreads * sizeof(E))
+        *reinterpret_cast<E*>(to + b) =
+            elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ GradTable<CAP> tab,
+__global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_constant__ GradTable<CAP> tab,
                                                          const double* __restrict__ partial, int n_partial,
                                                          const double* __restrict__ sumsq, float max_norm, float eps,
                                                          float* __restrict__ norm_out) {
     __shared__ double sh[kThreads / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums (see launch_scale)
     const double s = sumsq ? *sumsq : sum_partials(partial, n_partial, sh);
     const double norm = sqrt(s);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     const double ratio = static_cast<double>(max_norm) / (norm + static_cast<double>(eps));
     const float f = ratio >= 1. || norm == 0. ? 1.f : static_cast<float>(ratio);  // NaN stays NaN
     const int chunks = tab.first[tab.n];
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    for (int b = blockIdx.x; b < chunks; b += gridDim.x) {
+        const int c = chunks - 1 - b;  // the last ones first: they may still be in L2 from the sum
         const int i = tensor_of(tab, c);
         const long k = c - tab.first[i], n = tab.numel_type[i] >> 2;
         if (f == 1.f && tab.src[i] == tab.dst[i]) continue;  // in place, nothing to clip
@@ -198,7 +232,10 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     }
 }
 
+// Tensors of a launch: the table is 28 bytes for each and a kernel's parameters
+// hold 32,764.  Up to kFew tensors travel in a small table.
 constexpr int kCap = 1000;
+constexpr int kFew = 32;
 
 long chunks_of(const moe_tensor_ref& r) {
     if (r.numel == 0) return 0;
@@ -243,13 +280,15 @@ bool grad_chunks_fit(const moe_tensor_ref* refs, int n) {
     return true;
 }
 
-static cudaError_t launch_partials(const moe_tensor_ref* refs, int n, double* partial, int* n_partial,
-                                   cudaStream_t stream) {
-    GradTable<kCap> tab;
+namespace {
+
+template <int CAP>
+cudaError_t launch_partials(const moe_tensor_ref* refs, int n, double* partial, int* n_partial, cudaStream_t stream) {
+    GradTable<CAP> tab;
     *n_partial = 0;
     for (int at = 0; fill(&tab, refs, n, &at);) {
         const int grid = grid_of(tab.first[tab.n]);
-        sumsq_kernel<kCap><<<grid, kThreads, 0, stream>>>(tab, partial + *n_partial);
+        sumsq_kernel<CAP><<<grid, kThreads, 0, stream>>>(tab, partial + *n_partial);
         *n_partial += grid;
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
@@ -257,37 +296,62 @@ static cudaError_t launch_partials(const moe_tensor_ref* refs, int n, double* pa
     return cudaSuccess;
 }
 
+// The kernel is launched as a programmatic dependent of the one before it, so
+// that its blocks are in place when the sums are done; it waits for all of
+// that kernel before it reads or writes anything.
+template <int CAP>
+cudaError_t launch_scale(const GradTable<CAP>& tab, int grid, const double* partial, int n_partial,
+                         const double* sumsq, float max_norm, float eps, float* norm, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, scale_kernel<CAP>, tab, partial, n_partial, sumsq, max_norm, eps, norm);
+}
+
+template <int CAP>
+cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps, float* norm,
+                        double* partial, cudaStream_t stream) {
+    int np = 0;
+    if (!sumsq) {
+        cudaError_t e = launch_partials<CAP>(refs, n, partial, &np, stream);
+        if (e != cudaSuccess) return e;
+    }
+    GradTable<CAP> tab;
+    bool any = false;
+    for (int at = 0; fill(&tab, refs, n, &at); any = true) {
+        cudaError_t e = launch_scale(tab, grid_of(tab.first[tab.n]), partial, np, sumsq, max_norm, eps,
+                                     any ? nullptr : norm, stream);
+        if (e != cudaSuccess) return e;
+    }
+    // No values: the norm alone.
+    if (!any && norm) return launch_scale(tab, 1, partial, np, sumsq, max_norm, eps, norm, stream);
+    return cudaSuccess;
+}
+
+}  // namespace
+
 cudaError_t launch_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, float* norm, void* ws,
                               cudaStream_t stream) {
     int np = 0;
-    cudaError_t e = launch_partials(refs, n, static_cast<double*>(ws), &np, stream);
+    double* partial = static_cast<double*>(ws);
+    cudaError_t e = n <= kFew ? launch_partials<kFew>(refs, n, partial, &np, stream)
+                              : launch_partials<kCap>(refs, n, partial, &np, stream);
     if (e != cudaSuccess) return e;
-    finish_kernel<<<1, kThreads, 0, stream>>>(static_cast<double*>(ws), np, sumsq, norm);
+    finish_kernel<<<1, kThreads, 0, stream>>>(partial, np, sumsq, norm);
     return cudaGetLastError();
 }
 
 cudaError_t launch_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps,
                              float* norm, void* ws, cudaStream_t stream) {
-    int np = 0;
-    if (!sumsq) {
-        cudaError_t e = launch_partials(refs, n, static_cast<double*>(ws), &np, stream);
-        if (e != cudaSuccess) return e;
-    }
-    GradTable<kCap> tab;
-    bool any = false;
-    for (int at = 0; fill(&tab, refs, n, &at); any = true) {
-        scale_kernel<kCap><<<grid_of(tab.first[tab.n]), kThreads, 0, stream>>>(
-            tab, static_cast<const double*>(ws), np, sumsq, max_norm, eps, any ? nullptr : norm);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    if (!any && norm) {  // no values: the norm alone
-        tab.n = 0;
-        tab.first[0] = 0;
-        scale_kernel<kCap><<<1, kThreads, 0, stream>>>(tab, static_cast<const double*>(ws), np, sumsq, max_norm, eps, norm);
-        return cudaGetLastError();
-    }
-    return cudaSuccess;
+    double* partial = static_cast<double*>(ws);
+    return n <= kFew ? launch_clip<kFew>(refs, n, sumsq, max_norm, eps, norm, partial, stream)
+                     : launch_clip<kCap>(refs, n, sumsq, max_norm, eps, norm, partial, stream);
 }
 
 }  // namespace moe

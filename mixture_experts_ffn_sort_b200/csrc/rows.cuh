@@ -8,81 +8,116 @@
 
 namespace moe {
 
-// V bytes as one load or store.
-template <int V>
-struct RawVec;
-template <>
-struct RawVec<16> {
-    using type = uint4;
-};
-template <>
-struct RawVec<8> {
-    using type = uint2;
-};
-template <>
-struct RawVec<4> {
-    using type = uint32_t;
-};
-template <>
-struct RawVec<2> {
-    using type = uint16_t;
-};
-template <int V>
-using raw_t = typename RawVec<V>::type;
-
 __device__ __forceinline__ float elem_to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float elem_to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float elem_to_float(float v) { return v; }
 
-// V bytes of elements -> fp32 values, and back with one rounding each.
-template <class E, int V>
-__device__ __forceinline__ void unpack(const raw_t<V>& raw, float (&f)[V / sizeof(E)]) {
-    constexpr int N = V / sizeof(E);
-    E e[N];
-    memcpy(e, &raw, V);
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = elem_to_float(e[i]);
-}
+template <class E>
+__device__ __forceinline__ E elem_from_float(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 elem_from_float(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half elem_from_float(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ float elem_from_float(float v) { return v; }
 
-__device__ __forceinline__ void pair_to(__nv_bfloat162* o, float a, float b) { *o = __floats2bfloat162_rn(a, b); }
-__device__ __forceinline__ void pair_to(__half2* o, float a, float b) { *o = __floats2half2_rn(a, b); }
+// 16 bytes of elements -> fp32 values, and back with one rounding each.
+template <class E>
+constexpr int kVec = 16 / static_cast<int>(sizeof(E));
 
 template <class E>
-struct PairOf;
-template <>
-struct PairOf<__nv_bfloat16> {
-    using type = __nv_bfloat162;
-    static __device__ __forceinline__ __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct PairOf<__half> {
-    using type = __half2;
-    static __device__ __forceinline__ __half one(float v) { return __float2half_rn(v); }
-};
-
-template <class E, int V>
-__device__ __forceinline__ raw_t<V> pack(const float (&f)[V / sizeof(E)]) {
-    constexpr int N = V / sizeof(E);
-    raw_t<V> raw;
-    if constexpr (sizeof(E) == 4) {
-        memcpy(&raw, f, V);
-    } else if constexpr (N == 1) {
-        const E e = PairOf<E>::one(f[0]);
-        memcpy(&raw, &e, V);
-    } else {
-        typename PairOf<E>::type e[N / 2];
+__device__ __forceinline__ void unpack(const uint4& raw, float (&f)[kVec<E>]) {
+    E e[kVec<E>];
+    memcpy(e, &raw, 16);
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) pair_to(&e[i], f[2 * i], f[2 * i + 1]);
-        memcpy(&raw, e, V);
-    }
-    return raw;
+    for (int i = 0; i < kVec<E>; ++i) f[i] = elem_to_float(e[i]);
 }
 
-template <int V>
-__device__ __forceinline__ raw_t<V> zero_raw() {
-    raw_t<V> z;
-    memset(&z, 0, V);
-    return z;
+__device__ __forceinline__ uint4 pack_as(const float (&f)[8], __nv_bfloat16) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 pack_as(const float (&f)[8], __half) {
+    __half2 h[4];
+    uint4 raw;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    memcpy(&raw, h, 16);
+    return raw;
+}
+__device__ __forceinline__ uint4 pack_as(const float (&f)[4], float) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+template <class E>
+__device__ __forceinline__ uint4 pack(const float (&f)[kVec<E>]) {
+    return pack_as(f, E{});
+}
+
+// i / d for i * d < 2^63, d < 2^31: the high half of a product with
+// M = ceil(2^64 / d).  M d - 2^64 = e < d, so i M / 2^64 exceeds i / d by
+// i e / (d 2^64) < 1 / d, too little to reach the next whole number.
+struct FastDiv {
+    unsigned long long magic;  // 0: d == 1
+    unsigned d;
+    __host__ explicit FastDiv(unsigned v) : magic(v == 1 ? 0 : ~0ull / v + 1), d(v) {}
+    __device__ __forceinline__ long div(long i) const {
+        return magic ? static_cast<long>(__umul64hi(static_cast<unsigned long long>(i), magic)) : i;
+    }
+};
+
+// ---------------------------------------------------------------- rows that do not start on 16 bytes
+//
+// When a row's bytes are no multiple of 16, rows start at every multiple of
+// their element.  The kernels then still move 16 bytes at a time: 16 bytes
+// from any place are two aligned loads and a shift, the second of them an L1
+// hit of the neighbouring thread's first.  Only the 16-byte blocks that
+// reach out of the whole tensor (its last one) are read element by element.
+
+__device__ __forceinline__ uint4 load_block(const char* base, long a, long total) {
+    if (a >= 0 && a + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base + a));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long b = a + 2 * i;
+        if (b >= 0 && b + 2 <= total)
+            w[i >> 1] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(base + b))) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Bytes [at, at + 16) of a tensor of `total` bytes at the 16-byte aligned
+// `base` (zeros outside of it).
+__device__ __forceinline__ uint4 load_window(const char* base, long at, long total) {
+    const long a = at & ~15L;
+    const int sh = static_cast<int>(at & 15);
+    const uint4 lo = load_block(base, a, total);
+    if (sh == 0) return lo;
+    const uint4 hi = load_block(base, a + 16, total);
+    uint32_t w0 = lo.x, w1 = lo.y, w2 = lo.z, w3 = lo.w, w4 = hi.x, w5 = hi.y;
+    if (sh & 8) {
+        w0 = lo.z; w1 = lo.w; w2 = hi.x; w3 = hi.y; w4 = hi.z; w5 = hi.w;
+    }
+    if (sh & 4) {
+        w0 = w1; w1 = w2; w2 = w3; w3 = w4; w4 = w5;
+    }
+    const int bits = (sh & 3) * 8;
+    return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
+                      __funnelshift_r(w3, w4, bits));
+}
+
+// Elements [from, to) of a vector to `p`, where element 0 belongs (aligned to
+// its element): one store when that is the whole vector and p is aligned.
+template <class E>
+__device__ __forceinline__ void store_part(char* p, const uint4& v, int from, int to) {
+    if (from <= 0 && to >= kVec<E> && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        *reinterpret_cast<uint4*>(p) = v;
+    } else {
+        E e[kVec<E>];
+        memcpy(e, &v, 16);
+#pragma unroll
+        for (int i = 0; i < kVec<E>; ++i)
+            if (i >= from && i < to) reinterpret_cast<E*>(p)[i] = e[i];
+    }
 }
 
 }  // namespace moe
