@@ -8,8 +8,8 @@ fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -396,73 +396,31 @@ def moe_combine(y_sorted: torch.Tensor, inv_route: torch.Tensor, y_shared: Optio
 # ---------------------------------------------------------------- training: rows sorted by expert and back
 
 MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16 = 0, 1, 2
-_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16}
 
 
-def _refuse(name: str, t: torch.Tensor, dtype, idx: int, shape):
-    if t.get_device() != idx or idx < 0:
-        raise ValueError("%s must be a CUDA tensor on the device of the call's first tensor" % name)
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, not %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    raise ValueError("%s must be contiguous" % name)
+_B = None
 
 
-def _adr(name: str, t: torch.Tensor, dtype, idx: int, shape) -> int:
-    """The address of a contiguous tensor of this type and shape on device idx."""
-    if t.dtype is not dtype or t.get_device() != idx or idx < 0 or t.shape != shape or not t.is_contiguous():
-        _refuse(name, t, dtype, idx, shape)
-    return t.data_ptr()
+def _calls():
+    """The module that binds the training calls (csrc/binding.cpp): argument
+    checks, allocation and call in one step.  Raises if it has not been built."""
+    global _B
+    if _B is None:
+        lib()
+        path = os.path.join(_HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("%s is missing: build it with "
+                               "`python -m mixture_experts_ffn_sort_b200.build`" % path)
+        from . import _binding as module
+        module.error_class(MoEError)
+        _B = module
+    return _B
 
 
-def _adr_n(name: str, t: torch.Tensor, dtype, idx: int, n: int) -> int:
-    """The same of a tensor of n elements in any shape."""
-    if t.dtype is not dtype or t.get_device() != idx or idx < 0 or t.numel() != n or not t.is_contiguous():
-        if t.numel() != n:
-            raise ValueError("%s holds %d values, expected %d" % (name, t.numel(), n))
-        _refuse(name, t, dtype, idx, t.shape)
-    return t.data_ptr()
-
-
-def _status_adr(status, idx: int) -> Optional[int]:
-    return None if status is None else _adr_n("status", status, torch.int32, idx, status.numel() or 1)
-
-
-def _in_use(expert_offsets: Optional[torch.Tensor], idx: int) -> Optional[int]:
-    """The address of expert_offsets[E], the number of sorted rows in use."""
-    if expert_offsets is None:
-        return None
-    n = expert_offsets.numel()
-    return _adr_n("expert_offsets", expert_offsets, torch.int32, idx, n or 1) + 4 * (n - 1)
-
-
-def _row_dtype(name: str, t: torch.Tensor) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError("%s must be bfloat16, float16 or float32, not %s" % (name, t.dtype))
-    if t.dim() != 2:
-        raise ValueError("%s must be a matrix of rows, not of shape %s" % (name, tuple(t.shape)))
-    return d
-
-
-def _raw_stream(idx: int, stream) -> Optional[int]:
-    """The current stream's handle when a call for tensors of device idx can run
-    right here; None when the device or the stream has to be switched first."""
-    if idx < 0:
-        raise ValueError("tensors must be CUDA tensors")
-    if stream is None and torch.cuda.current_device() == idx:
-        return torch._C._cuda_getCurrentRawStream(idx)
-    return None
-
-
-def _there(idx: int, stream):
-    """A context in which device idx, and the given stream, are the current ones: the call's
-    launches and its allocations belong to them."""
-    if stream is None:
-        return torch.cuda.device(idx)
-    if stream.device.index != idx:
-        raise ValueError("the stream belongs to %s, the tensors to cuda:%d" % (stream.device, idx))
+def _on(stream, device: torch.device):
+    """The context of a call on `stream`: its launches and its allocations belong to it."""
+    if stream.device != device:
+        raise ValueError("the stream belongs to %s, the tensors to %s" % (stream.device, device))
     return torch.cuda.stream(stream)
 
 
@@ -473,32 +431,20 @@ def moe_permute(x: torch.Tensor, inv_route: torch.Tensor, expert_offsets: Option
     inv_route [T*K] -> x_sorted [T*K, H].  With moe_sort's expert_offsets the
     rows behind the last sorted one (routes that were skipped) are zeros;
     without it they are left as they were."""
-    idx = x.get_device()
-    s = _raw_stream(idx, stream)
-    if s is None:
-        with _there(idx, stream):
+    if stream is not None:
+        with _on(stream, x.device):
             return moe_permute(x, inv_route, expert_offsets, x_sorted, status)
-    dt, row = _row_dtype("x", x), x.dtype
-    T, H = x.shape
-    R = inv_route.numel()
-    K = R // T if T else 1
-    if R != T * K:
-        raise ValueError("inv_route holds %d positions: not a multiple of %d tokens" % (R, T))
-    if x_sorted is None:
-        x_sorted = x.new_empty((R, H))
-        out = x_sorted.data_ptr()
-    else:
-        out = _adr("x_sorted", x_sorted, row, idx, (R, H))
-    _check((_L or lib()).moe_permute(_adr_n("x", x, row, idx, T * H), _adr_n("inv_route", inv_route, torch.int32, idx, R),
-                                     _in_use(expert_offsets, idx), T, K, H, dt, out, _status_adr(status, idx), s))
-    return x_sorted
+    return (_B or _calls()).permute(x, inv_route, expert_offsets, x_sorted, status)
 
 
 def moe_permute_bwd(dx_sorted: torch.Tensor, inv_route: torch.Tensor, T: int, dx: Optional[torch.Tensor] = None,
                     status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient of moe_permute: dx_sorted [T*K, H] -> dx [T, H], each
     token's rows added in fp32 in slot order (moe_unpermute without weights)."""
-    return _unpermute(dx_sorted, inv_route, None, None, T, dx, status, stream)
+    if stream is not None:
+        with _on(stream, dx_sorted.device):
+            return moe_permute_bwd(dx_sorted, inv_route, T, dx, status)
+    return (_B or _calls()).unpermute(dx_sorted, inv_route, None, None, T, dx, status)
 
 
 def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch.Tensor,
@@ -508,31 +454,10 @@ def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch
     y_sorted [T*K, H] (bf16, f16 or f32), topk_w [T, K] f32 (and y_shared
     [T, H]) -> out [T, H], summed in fp32.  (moe_combine takes rows that carry
     their weight already.)"""
-    return _unpermute(y_sorted, inv_route, topk_w, y_shared, topk_w.shape[0], out, status, stream)
-
-
-def _unpermute(y_sorted, inv_route, topk_w, y_shared, T, out, status, stream):
-    idx = y_sorted.get_device()
-    s = _raw_stream(idx, stream)
-    if s is None:
-        with _there(idx, stream):
-            return _unpermute(y_sorted, inv_route, topk_w, y_shared, T, out, status, None)
-    dt, row = _row_dtype("sorted rows", y_sorted), y_sorted.dtype
-    R, H = y_sorted.shape
-    K = R // T if T else 1
-    if R != T * K:
-        raise ValueError("%d sorted rows: not a multiple of %d tokens" % (R, T))
-    if out is None:
-        out = y_sorted.new_empty((T, H))
-        to = out.data_ptr()
-    else:
-        to = _adr("out", out, row, idx, (T, H))
-    _check((_L or lib()).moe_unpermute(_adr_n("sorted rows", y_sorted, row, idx, R * H),
-                                       _adr_n("inv_route", inv_route, torch.int32, idx, R),
-                                       None if topk_w is None else _adr_n("topk_w", topk_w, torch.float32, idx, R),
-                                       None if y_shared is None else _adr("y_shared", y_shared, row, idx, (T, H)),
-                                       T, K, H, dt, to, _status_adr(status, idx), s))
-    return out
+    if stream is not None:
+        with _on(stream, y_sorted.device):
+            return moe_unpermute(y_sorted, inv_route, topk_w, y_shared, out, status)
+    return (_B or _calls()).unpermute(y_sorted, inv_route, topk_w, y_shared, topk_w.size(0), out, status)
 
 
 def moe_unpermute_bwd(dout: torch.Tensor, y_sorted: Optional[torch.Tensor], inv_route: torch.Tensor,
@@ -543,51 +468,12 @@ def moe_unpermute_bwd(dout: torch.Tensor, y_sorted: Optional[torch.Tensor], inv_
     dtopk_w [T, K] f32), None in the place of one that is not needed (y_sorted
     may be None when need_dw is False).  Rows behind the last sorted one as in
     moe_permute."""
-    idx = dout.get_device()
-    s = _raw_stream(idx, stream)
-    if s is None:
-        with _there(idx, stream):
+    if stream is not None:
+        with _on(stream, dout.device):
             return moe_unpermute_bwd(dout, y_sorted, inv_route, topk_w, expert_offsets, need_dy, need_dw, dy_sorted,
                                      dtopk_w, status)
-    dt, row = _row_dtype("dout", dout), dout.dtype
-    T, H = dout.shape
-    if topk_w.dim() != 2 or topk_w.shape[0] != T:
-        raise ValueError("topk_w must be [%d, K], not %s" % (T, tuple(topk_w.shape)))
-    R = topk_w.numel()
-    K = topk_w.shape[1]
-    if not (need_dy or need_dw):
-        return None, None
-    dy = dw = y = None
-    if not need_dy:
-        dy_sorted = None
-    elif dy_sorted is None:
-        dy_sorted = dout.new_empty((R, H))
-        dy = dy_sorted.data_ptr()
-    else:
-        dy = _adr("dy_sorted", dy_sorted, row, idx, (R, H))
-    if not need_dw:
-        dtopk_w = None
-    else:
-        if y_sorted is None:
-            raise ValueError("the weights' gradient needs y_sorted")
-        y = _adr("y_sorted", y_sorted, row, idx, (R, H))
-        if dtopk_w is None:
-            dtopk_w = topk_w.new_empty((T, K))
-            dw = dtopk_w.data_ptr()
-        else:
-            dw = _adr("dtopk_w", dtopk_w, torch.float32, idx, (T, K))
-    _check((_L or lib()).moe_unpermute_bwd(_adr_n("dout", dout, row, idx, T * H), y,
-                                           _adr_n("inv_route", inv_route, torch.int32, idx, R),
-                                           _adr_n("topk_w", topk_w, torch.float32, idx, R),
-                                           _in_use(expert_offsets, idx), T, K, H, dt, dy, dw,
-                                           _status_adr(status, idx), s))
-    return dy_sorted, dtopk_w
-
-
-@functools.lru_cache(maxsize=64)
-def _score_config(score: int, n_group: int, topk_group: int, renormalize: int, scaling: float):
-    """A routing configuration without a bias, read by the library only."""
-    return ctypes.pointer(_RouteConfig(score, None, n_group, topk_group, renormalize, scaling))
+    return (_B or _calls()).unpermute_bwd(dout, y_sorted, inv_route, topk_w, expert_offsets, need_dy, need_dw,
+                                            dy_sorted, dtopk_w, status)
 
 
 def moe_route_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.Tensor,
@@ -599,49 +485,15 @@ def moe_route_bwd(logits: torch.Tensor, topk_ids: torch.Tensor, dtopk_w: torch.T
     [T, K] f32 -> dlogits [T, E] f32, the choice topk_ids held fixed.  Takes the
     routing call's keyword arguments; sel_bias and the groups only choose, so
     they take no part."""
-    idx = logits.get_device()
-    s = _raw_stream(idx, stream)
-    if s is None:
-        with _there(idx, stream):
+    if stream is not None:
+        with _on(stream, logits.device):
             return moe_route_bwd(logits, topk_ids, dtopk_w, score, sel_bias, n_group, topk_group, renormalize,
                                  scaling, zero_mask, dlogits, status)
-    if logits.dim() != 2 or topk_ids.dim() != 2:
-        raise ValueError("logits must be [T, E] and topk_ids [T, K]")
-    T, E = logits.shape
-    K = topk_ids.shape[1]
-    f32 = torch.float32
-    mask = None
-    if zero_mask is not None:
-        if zero_mask.dtype is torch.bool:
-            zero_mask = zero_mask.view(torch.uint8)
-        mask = _adr("zero_mask", zero_mask, torch.uint8, idx, (T, K))
-    if dlogits is None:
-        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
-        out = dlogits.data_ptr()
-    else:
-        out = _adr("dlogits", dlogits, f32, idx, (T, E))
-    cfg = _score_config(int(score), int(n_group), int(n_group if topk_group is None else topk_group),
-                        int(bool(renormalize)), float(scaling))
-    _check((_L or lib()).moe_route_bwd(_adr("logits", logits, f32, idx, (T, E)),
-                                       _adr("topk_ids", topk_ids, torch.int32, idx, (T, K)),
-                                       _adr("dtopk_w", dtopk_w, f32, idx, (T, K)), T, E, K, cfg, mask, out,
-                                       _status_adr(status, idx), s))
-    return dlogits
+    return (_B or _calls()).route_bwd(logits, topk_ids, dtopk_w, score, n_group, topk_group, renormalize, scaling,
+                                        zero_mask, dlogits, status)
 
 
 # ---------------------------------------------------------------- training: gradient norm and clipping
-
-def _dense(t: torch.Tensor) -> bool:
-    """Whether the elements fill one stretch of memory, in any order of the dimensions."""
-    if t.is_contiguous():
-        return True
-    step = 1
-    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
-        if stride != step:
-            return False
-        step *= size
-    return True
-
 
 class TensorList:
     """Gradient tensors as moe_grad_norm, moe_grad_sumsq and moe_grad_clip take
@@ -654,64 +506,37 @@ class TensorList:
     def __init__(self, tensors, out=None, device=None):
         self.tensors = list(tensors)
         self.out = self.tensors if out is None else list(out)
-        if len(self.out) != len(self.tensors):
-            raise ValueError("%d tensors but %d outputs" % (len(self.tensors), len(self.out)))
-        n = len(self.tensors)
-        if n:
+        if self.tensors:
             device = self.tensors[0].device
         device = torch.device("cuda" if device is None else device)
-        if device.type == "cuda" and device.index is None:
-            device = torch.device("cuda", torch.cuda.current_device())
-        self.device, self.n = device, n
-        self.refs = (_TensorRef * max(n, 1))()
-        for i, (t, o) in enumerate(zip(self.tensors, self.out)):
-            dt = _DTYPES.get(t.dtype)
-            if dt is None:
-                raise ValueError("tensor %d must be bfloat16, float16 or float32, not %s" % (i, t.dtype))
-            if not t.is_cuda or t.device != self.device or o.device != self.device:
-                raise ValueError("tensor %d: the tensors and outputs must be CUDA tensors on one device" % i)
-            if o is not t and (o.dtype != t.dtype or o.shape != t.shape or (t.numel() and o.stride() != t.stride())):
-                raise ValueError("output %d must have the shape, strides and type of its tensor" % i)
-            if not _dense(t):
-                raise ValueError("tensor %d must be dense in memory (strides %s)" % (i, t.stride()))
-            self.refs[i] = _TensorRef(t.data_ptr(), o.data_ptr(), t.numel(), dt, 0)
-        _check(lib().moe_grad_refs_check(self.refs, n))
-        self.workspace_bytes = int(lib().moe_grad_workspace_bytes(n))
-        # What the calls allocate their results and workspaces from (each call its own).
-        self.index = self.device.index
-        self.none32 = torch.empty(0, dtype=torch.float32, device=self.device)
-        self.none64 = torch.empty(0, dtype=torch.float64, device=self.device)
+        if device.type != "cuda":
+            raise ValueError("the tensors must be CUDA tensors")
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        self.refs = (_B or _calls()).refs(self.tensors, self.out, self.device.index)
 
 
-def _tensor_list(tensors) -> TensorList:
-    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+def _refs_on(tensors, stream):
+    tl = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+    return tl, None if stream is None else _on(stream, tl.device)
 
 
 def moe_grad_sumsq(tensors, stream=None, norm: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The sum of squares over all tensors, f64 [] on the device (what ranks that
     hold different tensors add up before moe_grad_clip).  tensors: a
     TensorList or a sequence of tensors.  norm: an f32 [] that receives the root."""
-    tl = _tensor_list(tensors)
-    s = _raw_stream(tl.index, stream)
-    if s is None:
-        with _there(tl.index, stream):
-            return moe_grad_sumsq(tl, None, norm)
-    sumsq = tl.none64.new_empty(())
-    ws = tl.none64.new_empty(tl.workspace_bytes // 8)
-    _check((_L or lib()).moe_grad_sumsq(tl.refs, tl.n, sumsq.data_ptr(),
-                                        None if norm is None else _adr("norm", norm, torch.float32, tl.index, ()),
-                                        ws.data_ptr(), tl.workspace_bytes, s))
-    return sumsq
+    tl, on = _refs_on(tensors, stream)
+    if on is not None:
+        with on:
+            return _B.grad_sumsq(tl.refs, norm)
+    return _B.grad_sumsq(tl.refs, norm)
 
 
 def moe_grad_norm(tensors, stream=None) -> torch.Tensor:
     """The 2-norm over all tensors as one vector, f32 [] on the device."""
-    tl = _tensor_list(tensors)
-    if _raw_stream(tl.index, stream) is None:
-        with _there(tl.index, stream):
-            return moe_grad_norm(tl)
-    norm = tl.none32.new_empty(())
-    moe_grad_sumsq(tl, None, norm)
+    tl, on = _refs_on(tensors, stream)
+    with on or contextlib.nullcontext():
+        norm = torch.empty((), dtype=torch.float32, device=tl.device)
+        _B.grad_sumsq(tl.refs, norm)
     return norm
 
 
@@ -721,19 +546,11 @@ def moe_grad_clip(tensors, max_norm: float, eps: float = 1e-6, sumsq: Optional[t
     the list's outputs, and returns the norm before that, f32 [] on the device.
     sumsq: the f64 [] sum of squares to take the norm from (over more tensors
     than these, such as those of other ranks); None: of these tensors."""
-    tl = _tensor_list(tensors)
-    s = _raw_stream(tl.index, stream)
-    if s is None:
-        with _there(tl.index, stream):
-            return moe_grad_clip(tl, max_norm, eps, sumsq)
-    norm = tl.none32.new_empty(())
-    if sumsq is None:
-        ws = tl.none64.new_empty(tl.workspace_bytes // 8)
-        given, work, size = None, ws.data_ptr(), tl.workspace_bytes
-    else:
-        given, work, size = _adr_n("sumsq", sumsq, torch.float64, tl.index, 1), None, 0
-    _check((_L or lib()).moe_grad_clip(tl.refs, tl.n, given, max_norm, eps, norm.data_ptr(), work, size, s))
-    return norm
+    tl, on = _refs_on(tensors, stream)
+    if on is not None:
+        with on:
+            return _B.grad_clip(tl.refs, max_norm, eps, sumsq)
+    return _B.grad_clip(tl.refs, max_norm, eps, sumsq)
 
 
 # ---------------------------------------------------------------- whole layer

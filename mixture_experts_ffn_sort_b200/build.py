@@ -1,6 +1,7 @@
 """Build step of the CUDA library: compiles csrc/*.cu for sm_100a into
 libmoe_ffn_b200.so next to this file (static CUDA runtime, no libcuda link,
-so the library loads on a machine without a GPU driver).
+so the library loads on a machine without a GPU driver), and csrc/binding.cpp,
+the Python binding of the training calls, into _binding.so beside it.
 
     python -m mixture_experts_ffn_sort_b200.build [--force] [--verbose]
 """
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_ffn_b200.so")
+BINDING = os.path.join(HERE, "_binding.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,8 +44,37 @@ def _stale(target, deps):
 
 def build(force: bool = False, verbose: bool = False) -> str:
     deps = _deps()
-    if not force and not _stale(LIB, deps + [__file__]):
-        return LIB
+    if force or _stale(LIB, deps + [__file__]):
+        _build_library(deps, force, verbose)
+    binding = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_ffn.h"), __file__]
+    if force or _stale(BINDING, binding):
+        _build_binding(binding[0], verbose)
+    return LIB
+
+
+def _build_binding(src: str, verbose: bool):
+    """The host compiler on binding.cpp, against torch's headers and the library (found beside it when loaded)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += [a for i in inc for a in ("-isystem", i)]
+    cmd += [src, "-o", tmp, "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L",
+            os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the host compiler failed for %s:\n%s%s" % (src, r.stdout, r.stderr))
+    if verbose and r.stderr:
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, BINDING)
+
+
+def _build_library(deps, force: bool, verbose: bool):
     os.makedirs(OBJ_DIR, exist_ok=True)
     headers = [d for d in deps if not d.endswith(".cu")]
 
@@ -68,7 +99,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 def main():
