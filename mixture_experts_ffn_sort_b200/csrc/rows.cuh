@@ -53,6 +53,20 @@ __device__ __forceinline__ uint4 pack(const float (&f)[kVec<E>]) {
     return pack_as(f, E{});
 }
 
+// acc += w * elements, the fp32 additions two at a time.
+template <class E>
+__device__ __forceinline__ void add_weighted(float (&acc)[kVec<E>], const uint4& raw, float w) {
+    float f[kVec<E>];
+    unpack<E>(raw, f);
+#pragma unroll
+    for (int i = 0; i < kVec<E>; i += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\t"
+            "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+            : "+f"(acc[i]), "+f"(acc[i + 1])
+            : "f"(f[i]), "f"(f[i + 1]), "f"(w));
+}
+
 // i / d for i * d < 2^63, d < 2^31: the high half of a product with
 // M = ceil(2^64 / d).  M d - 2^64 = e < d, so i M / 2^64 exceeds i / d by
 // i e / (d 2^64) < 1 / d, too little to reach the next whole number.
@@ -85,14 +99,8 @@ __device__ __forceinline__ uint4 load_block(const char* base, long a, long total
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Bytes [at, at + 16) of a tensor of `total` bytes at the 16-byte aligned
-// `base` (zeros outside of it).
-__device__ __forceinline__ uint4 load_window(const char* base, long at, long total) {
-    const long a = at & ~15L;
-    const int sh = static_cast<int>(at & 15);
-    const uint4 lo = load_block(base, a, total);
-    if (sh == 0) return lo;
-    const uint4 hi = load_block(base, a + 16, total);
+// Bytes [sh, sh + 16) of two 16-byte blocks, 0 < sh < 16.
+__device__ __forceinline__ uint4 shift_blocks(const uint4& lo, const uint4& hi, int sh) {
     uint32_t w0 = lo.x, w1 = lo.y, w2 = lo.z, w3 = lo.w, w4 = hi.x, w5 = hi.y;
     if (sh & 8) {
         w0 = lo.z; w1 = lo.w; w2 = hi.x; w3 = hi.y; w4 = hi.z; w5 = hi.w;
@@ -103,6 +111,89 @@ __device__ __forceinline__ uint4 load_window(const char* base, long at, long tot
     const int bits = (sh & 3) * 8;
     return make_uint4(__funnelshift_r(w0, w1, bits), __funnelshift_r(w1, w2, bits), __funnelshift_r(w2, w3, bits),
                       __funnelshift_r(w3, w4, bits));
+}
+
+// Bytes [at, at + 16) of a tensor of `total` bytes at the 16-byte aligned
+// `base` (zeros outside of it).
+__device__ __forceinline__ uint4 load_window(const char* base, long at, long total) {
+    const long a = at & ~15L;
+    const int sh = static_cast<int>(at & 15);
+    const uint4 lo = load_block(base, a, total);
+    if (sh == 0) return lo;
+    return shift_blocks(lo, load_block(base, a + 16, total), sh);
+}
+
+// One row as the 4-byte words of memory that it touches: word k holds its
+// bytes [4 k - lead, 4 k - lead + 4), where lead is 2 for a row that starts
+// within a word (HALF: rows of an odd number of 2-byte elements) and 0 otherwise.
+template <bool HALF>
+struct RowWords {
+    const char* base;  // word 0
+    int row_bytes, lead;
+    long left;  // bytes of the tensor from word 0 on
+    __device__ __forceinline__ RowWords(const char* tensor, long row, long bytes, long total)
+        : row_bytes(static_cast<int>(bytes)) {
+        const long at = row * bytes;
+        lead = HALF ? static_cast<int>(at & 2) : 0;
+        base = tensor + (at - lead);
+        left = total - (at - lead);
+    }
+    __device__ __forceinline__ int count() const { return (row_bytes + lead + 3) >> 2; }
+    // Word k, 0 outside of 0 .. count(); its halves that belong to other rows are those rows'.
+    __device__ __forceinline__ uint32_t word(int k) const {
+        if (k < 0 || k >= count()) return 0;
+        if (!HALF || 4L * k + 4 <= left) return __ldg(reinterpret_cast<const uint32_t*>(base) + k);
+        return __ldg(reinterpret_cast<const uint16_t*>(base) + 2 * k);  // the tensor's last element
+    }
+    // Word k (given) as it is for a row of the other start.
+    __device__ __forceinline__ uint32_t shifted(int k, uint32_t same) const {
+        return lead ? __funnelshift_r(same, word(k + 1), 16) : __funnelshift_r(word(k - 1), same, 16);
+    }
+};
+
+// Word k of the row at byte `at` of a tensor (counted as in RowWords), without the halves outside the row.
+template <bool HALF>
+__device__ __forceinline__ void store_word(char* tensor, long at, long row_bytes, int k, uint32_t v) {
+    const int lead = HALF ? static_cast<int>(at & 2) : 0;
+    const int from = 4 * k - lead, bytes = static_cast<int>(row_bytes);
+    char* o = tensor + at + from;
+    if (from >= 0 && from + 4 <= bytes) {
+        *reinterpret_cast<uint32_t*>(o) = v;
+    } else if (HALF) {
+        if (from >= 0 && from + 2 <= bytes) *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(v);
+        if (from == -2) *reinterpret_cast<uint16_t*>(o + 2) = static_cast<uint16_t>(v >> 16);
+    }
+}
+
+// The words at + 128 k (k = 0..3) of shared memory at any 2-byte place `at` of
+// `base` (16-byte aligned, 4 bytes of room after the last word).
+__device__ __forceinline__ uint4 load_shared_words(const char* base, int at) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(base + (at & ~3));
+    uint4 v = make_uint4(p[0], p[32], p[64], p[96]);
+    if (at & 2) {
+        v.x = __funnelshift_r(v.x, p[1], 16);
+        v.y = __funnelshift_r(v.y, p[33], 16);
+        v.z = __funnelshift_r(v.z, p[65], 16);
+        v.w = __funnelshift_r(v.w, p[97], 16);
+    }
+    return v;
+}
+
+// Those words to p + 128 k (4-byte aligned), where p is byte `rel` of a row of `row_bytes`.
+template <class E>
+__device__ __forceinline__ void store_words(char* p, const uint4& v, long rel, long row_bytes) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const long r = rel + 128 * k;
+        char* o = p + 128 * k;
+        if (r >= 0 && r + 4 <= row_bytes) {
+            *reinterpret_cast<uint32_t*>(o) = w[k];
+        } else if (sizeof(E) == 2) {  // half a word at the row's first or last byte
+            if (r >= 0 && r + 2 <= row_bytes) *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(w[k]);
+            if (r + 2 >= 0 && r + 4 <= row_bytes) *reinterpret_cast<uint16_t*>(o + 2) = static_cast<uint16_t>(w[k] >> 16);
+        }
+    }
 }
 
 // Elements [from, to) of a vector to `p`, where element 0 belongs (aligned to

@@ -16,7 +16,10 @@ from _train_ref import DTYPES, HALF, TINY, U32
 pytestmark = pytest.mark.gpu
 
 SIZES = [(1, 1, 1, 1), (1, 2048, 8, 256), (7, 3, 2, 5), (33, 30, 4, 9), (64, 64, 8, 8), (130, 1030, 6, 64),
-         (5, 515, 32, 40), (257, 2048, 3, 16), (40, 4100, 9, 12), (3, 24, 17, 4)]
+         (5, 515, 32, 40), (257, 2048, 3, 16), (40, 4100, 9, 12), (3, 24, 17, 4),
+         # Long rows of many tokens, at every alignment.
+         (520, 1030, 6, 64), (1100, 515, 3, 8), (300, 4100, 9, 12), (129, 4097, 32, 40), (2100, 261, 2, 4),
+         (1030, 512, 17, 24)]
 
 
 def bits(t):
@@ -72,6 +75,49 @@ def test_unpermute_and_permute_bwd(T, H, K, E, drop, dtype):
     close(moe.moe_unpermute(y.cuda(), inv.cuda(), w.cuda(), x.cuda()), want, err, dtype)
     terms = ref.weighted(y, inv, None, T)
     close(moe.moe_permute_bwd(y.cuda(), inv.cuda(), T), terms.sum(1), (K + 2) * U32 * terms.abs().sum(1), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("drop", [0.0, 0.3, 0.97])
+@pytest.mark.parametrize("T,H,K,E", [
+    (1300, 4097, 5, 64), (2500, 1031, 10, 64), (3000, 514, 17, 40), (400, 2050, 32, 40), (12301, 2049, 1, 8),
+    (1100, 4096, 16, 32), (4099, 1024, 17, 40), (600, 8192, 32, 40), (8200, 2048, 4, 8), (2400, 5000, 7, 12)])
+def test_unpermute_of_many_long_rows(T, H, K, E, drop, dtype):
+    """64 MB and more, where the rows go through shared memory (24 MB for rows that do not
+    start on 16 bytes); against 64-bit sums on the GPU, slot by slot."""
+    _, off, inv = ref.routes(T, K, E, drop, T)
+    inv = inv.cuda()
+    g = torch.Generator(device="cuda").manual_seed(H)
+    y = torch.randn((T * K, H), generator=g, device="cuda").to(dtype)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dtype)
+    w = torch.rand((T, K), generator=g, device="cuda")
+    w[torch.rand((T, K), generator=g, device="cuda") < 0.05] = 0.0
+    y[int(off[-1]):] = math.nan  # behind the last row: not read
+    y[inv[(inv >= 0) & (w.view(-1) == 0)].long()] = math.inf  # hidden by a weight of 0
+    want = torch.zeros((T, H), dtype=torch.float64, device="cuda")
+    size, plain, plain_size = torch.zeros_like(want), torch.zeros_like(want), torch.zeros_like(want)
+    clean = torch.where(y.isfinite(), y, 0)
+    for j in range(K):
+        p = inv.view(T, K)[:, j]
+        rows = torch.where((p >= 0)[:, None], clean[p.clamp(min=0).long()].double(), 0.0)
+        plain += rows
+        plain_size += rows.abs()
+        want += rows * w[:, j, None]
+        size += rows.abs() * w[:, j, None]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for got, exp, mag in ((moe.moe_unpermute(y, inv, w, status=status), want, size),
+                          (moe.moe_unpermute(y, inv, w, x, status=status), want + x.double(), size + x.double().abs()),
+                          (moe.moe_permute_bwd(clean, inv, T, status=status), plain, plain_size)):
+        err = (K + 2) * U32 * mag
+        bound = HALF[dtype] * (exp.abs() + err) + err + TINY[dtype]
+        assert ((got.double() - exp).abs() <= bound).all()
+    assert status.item() == 0
+    # Corrupt positions among them.
+    bad = inv.clone()
+    bad[5], bad[T * K - 1], bad[T * K // 2] = T * K, -7, 2 ** 31 - 1
+    cut = torch.where((bad < 0) | (bad >= T * K), -1, bad)
+    assert torch.equal(moe.moe_permute_bwd(clean, bad, T, status=status), moe.moe_permute_bwd(clean, cut, T))
+    assert status.item() == moe.MOE_STATUS_BAD_MAP
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
