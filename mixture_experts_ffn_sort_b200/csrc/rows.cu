@@ -22,6 +22,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // slots of a token whose rows are in flight together
 
 // The sorted position of a route, or -1; flags corrupt entries.
 __device__ __forceinline__ int32_t position(const int32_t* __restrict__ inv, long r, long R, bool* bad) {
@@ -95,7 +96,11 @@ __global__ void __launch_bounds__(kThreads) permute_words_kernel(const char* __r
 #pragma unroll
         for (int u = 0; u < W; ++u) {
             same[u] = src.word(k0 + 32 * u);
-            if (HALF) other[u] = src.shifted(k0 + 32 * u, same[u]);
+            if (HALF) other[u] = src.beside(k0 + 32 * u);
+        }
+        if (HALF) {
+#pragma unroll
+            for (int u = 0; u < W; ++u) other[u] = src.shifted(same[u], other[u]);
         }
 #pragma unroll 2
         for (int j = 0; j < K; ++j) {
@@ -111,13 +116,29 @@ __global__ void __launch_bounds__(kThreads) permute_words_kernel(const char* __r
     if (bad) report_status(status, MOE_STATUS_BAD_MAP);
 }
 
-// Slots of a batch at most.
-constexpr int kBatch = 4;
+
+// The positions and weights of slots j0 .. j0 + n of a token, -1 for those that
+// add nothing.
+template <int B>
+__device__ __forceinline__ void slot_batch(const int32_t* __restrict__ inv, const float* __restrict__ w, long r, long R,
+                                           int n, int32_t (&p)[B], float (&wj)[B], bool* bad) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        p[b] = -1;
+        wj[b] = 1.f;
+        if (b < n) {
+            p[b] = position(inv, r + b, R, bad);
+            if (w) wj[b] = __ldg(w + r + b);
+            if (wj[b] == 0.f) p[b] = -1;
+        }
+    }
+}
 
 // out[t] = sum_j w[t, j] y[inv[t, j]] (+ y_shared[t]).  One thread per 16-byte
 // column of a token; slots in batches: all positions, then all rows, then the
-// sums in slot order, so that the loads of a batch are in flight together.
-template <class E, bool SHIFT>
+// sums in slot order, so that the loads of a batch (of at most B) are in flight
+// together.  SHIFT: rows that start anywhere, by shifted windows.
+template <class E, bool SHIFT, int B>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restrict__ y_sorted,
                                                              const int32_t* __restrict__ inv,
                                                              const float* __restrict__ w,
@@ -125,7 +146,6 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
                                                              int batch, long row_bytes, const FastDiv vecs,
                                                              char* __restrict__ out, int32_t* __restrict__ status) {
     constexpr int N = kVec<E>;
-    constexpr int B = kBatch;
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * vecs.d;
     bool bad = false;
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
@@ -135,19 +155,9 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
 #pragma unroll
         for (int n = 0; n < N; ++n) acc[n] = 0.f;
         for (int j0 = 0; j0 < K; j0 += batch) {
-            const int n_here = K - j0 < batch ? K - j0 : batch;
             int32_t p[B];
             float wj[B];
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                p[b] = -1;
-                wj[b] = 1.f;
-                if (b < n_here) {
-                    p[b] = position(inv, t * K + j0 + b, R, &bad);
-                    if (w) wj[b] = __ldg(w + t * K + j0 + b);
-                    if (wj[b] == 0.f) p[b] = -1;
-                }
-            }
+            slot_batch(inv, w, t * K + j0, R, K - j0 < batch ? K - j0 : batch, p, wj, &bad);
             uint4 v[B];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
@@ -157,9 +167,8 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
                 else v[b] = __ldg(reinterpret_cast<const uint4*>(y_sorted + row) + c);
             }
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
+            for (int b = 0; b < B; ++b)
                 if (p[b] >= 0) add_weighted<E>(acc, v[b], wj[b]);
-            }
         }
         const long at = t * row_bytes + 16 * c;
         if (y_shared) {
@@ -171,6 +180,66 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
         }
         if (SHIFT) store_part<E>(out + at, pack<E>(acc), 0, static_cast<int>((row_bytes - 16 * c) / sizeof(E)));
         else *reinterpret_cast<uint4*>(out + at) = pack<E>(acc);
+    }
+    if (bad) report_status(status, MOE_STATUS_BAD_MAP);
+}
+
+// The same for rows of a multiple of 4 bytes but not 16, by 4-byte words; a
+// thread has W of them, a warp's width apart.
+template <class E, int W>
+__global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* __restrict__ y_sorted,
+                                                                   const int32_t* __restrict__ inv,
+                                                                   const float* __restrict__ w,
+                                                                   const char* __restrict__ y_shared, int T, int K,
+                                                                   int batch, long row_bytes, const FastDiv tiles,
+                                                                   char* __restrict__ out,
+                                                                   int32_t* __restrict__ status) {
+    constexpr int B = kBatch;
+    const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * tiles.d * (W > 1 ? 32 : 1);
+    const int words = static_cast<int>(row_bytes >> 2);
+    bool bad = false;
+    for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<long>(gridDim.x) * blockDim.x) {
+        const long tile = W > 1 ? i >> 5 : i, t = tiles.div(tile);
+        const int k0 = static_cast<int>(tile - t * tiles.d) * (W > 1 ? 32 * W : 1) + (W > 1 ? threadIdx.x & 31 : 0);
+        auto load = [&](const char* row, uint32_t (&v)[W]) {
+#pragma unroll
+            for (int u = 0; u < W; ++u)
+                v[u] = k0 + 32 * u < words ? __ldg(reinterpret_cast<const uint32_t*>(row) + k0 + 32 * u) : 0;
+        };
+        float acc[W][2];
+#pragma unroll
+        for (int u = 0; u < W; ++u) acc[u][0] = acc[u][1] = 0.f;
+        auto add = [&](const uint32_t (&v)[W], float by) {
+#pragma unroll
+            for (int u = 0; u < W; ++u) {
+                float f[2];
+                unpack_word<E>(v[u], f);
+                acc[u][0] = fmaf(by, f[0], acc[u][0]);
+                acc[u][1] = fmaf(by, f[1], acc[u][1]);
+            }
+        };
+        for (int j0 = 0; j0 < K; j0 += batch) {
+            int32_t p[B];
+            float wj[B];
+            slot_batch(inv, w, t * K + j0, R, K - j0 < batch ? K - j0 : batch, p, wj, &bad);
+            uint32_t v[B][W];
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                if (p[b] >= 0) load(y_sorted + p[b] * row_bytes, v[b]);
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+                if (p[b] >= 0) add(v[b], wj[b]);
+        }
+        if (y_shared) {
+            uint32_t v[W];
+            load(y_shared + t * row_bytes, v);
+            add(v, 1.f);
+        }
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+            if (k0 + 32 * u < words)
+                reinterpret_cast<uint32_t*>(out + t * row_bytes)[k0 + 32 * u] = pack_word<E>(acc[u]);
     }
     if (bad) report_status(status, MOE_STATUS_BAD_MAP);
 }
@@ -608,6 +677,20 @@ int grid_for(long threads) {
 
 long row_bytes_of(const RowsArgs& a) { return static_cast<long>(a.H) * dtype_bytes(a.dtype); }
 
+// The words of a row at either start (RowWords), in tiles of one, or of four to
+// a lane of a warp when that leaves no warp short.
+struct WordTiles {
+    bool four;
+    FastDiv div;  // tiles of a row
+    int grid;
+    WordTiles(const RowsArgs& a, long row) : div(1) {
+        const long words = (row + (row % 4 ? 2 : 0) + 3) / 4;
+        four = words >= 128;
+        div = FastDiv(static_cast<unsigned>(four ? (words + 127) / 128 : words));
+        grid = grid_for(static_cast<long>(a.T) * div.d * (four ? 32 : 1));
+    }
+};
+
 template <int V>
 using Int = std::integral_constant<int, V>;
 
@@ -634,17 +717,13 @@ cudaError_t launch_permute(const RowsArgs& a, const void* x, void* x_sorted, cud
             in, a.inv, a.n_rows, a.T, a.K, row, vecs, out, a.status);
         return cudaGetLastError();
     }
-    // Words of a row at either start; four of them to a thread when that leaves no warp short.
-    const long words = (row + (row % 4 ? 2 : 0) + 3) / 4;
-    const bool four = words >= 128;
-    const FastDiv tiles(static_cast<unsigned>(four ? (words + 127) / 128 : words));
-    const int grid = grid_for(static_cast<long>(a.T) * tiles.d * (four ? 32 : 1));
+    const WordTiles tiles(a, row);
     auto launch = [&](auto half, auto w) {
-        permute_words_kernel<decltype(half)::value, decltype(w)::value><<<grid, kThreads, 0, stream>>>(
-            in, a.inv, a.n_rows, a.T, a.K, row, tiles, out, a.status);
+        permute_words_kernel<decltype(half)::value, decltype(w)::value><<<tiles.grid, kThreads, 0, stream>>>(
+            in, a.inv, a.n_rows, a.T, a.K, row, tiles.div, out, a.status);
     };
-    if (row % 4) four ? launch(std::true_type{}, Int<4>{}) : launch(std::true_type{}, Int<1>{});
-    else four ? launch(std::false_type{}, Int<4>{}) : launch(std::false_type{}, Int<1>{});
+    if (row % 4) tiles.four ? launch(std::true_type{}, Int<4>{}) : launch(std::true_type{}, Int<1>{});
+    else tiles.four ? launch(std::false_type{}, Int<4>{}) : launch(std::false_type{}, Int<1>{});
     return cudaGetLastError();
 }
 
@@ -694,14 +773,38 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* y_sorted, const floa
     const long row = row_bytes_of(a);
     if (row >= kRingMinRow && a.T * a.K * row >= (row % 16 ? kRingMinBytesShift : kRingMinBytes))
         return launch_unpermute_ring(a, y_sorted, w, y_shared, out, stream);
-    const FastDiv vecs(static_cast<unsigned>((row + 15) / 16));
-    const int grid = grid_for(static_cast<long>(a.T) * vecs.d);
+    const char *y = static_cast<const char*>(y_sorted), *sh = static_cast<const char*>(y_shared);
+    char* to = static_cast<char*>(out);
+    auto even = [&](int most) { return (a.K + (a.K + most - 1) / most - 1) / ((a.K + most - 1) / most); };
     dispatch(a, [&](auto e, auto shift) {
-        constexpr int B = kBatch;
-        const int batches = (a.K + B - 1) / B, batch = (a.K + batches - 1) / batches;
-        unpermute_kernel<decltype(e), decltype(shift)::value><<<grid, kThreads, 0, stream>>>(
-            static_cast<const char*>(y_sorted), a.inv, w, static_cast<const char*>(y_shared), a.T, a.K, batch, row,
-            vecs, static_cast<char*>(out), a.status);
+        using E = decltype(e);
+        const FastDiv vecs(static_cast<unsigned>((row + 15) / 16));
+        const int grid = grid_for(static_cast<long>(a.T) * vecs.d);
+        auto vectors = [&](auto sh_, auto most) {
+            constexpr int B = decltype(most)::value;
+            unpermute_kernel<E, decltype(sh_)::value, B><<<grid, kThreads, 0, stream>>>(y, a.inv, w, sh, a.T, a.K,
+                                                                                      even(B), row, vecs, to, a.status);
+        };
+        if constexpr (!decltype(shift)::value) {
+            // One wave of blocks: one batch of all slots is one wait less (64 tokens of width 2048,
+            // top-8: 2.6 us against 2.8 us).  More: the registers of larger batches cost more warps
+            // than the wait.
+            if (a.K > 4 && grid <= 148 * 3) vectors(shift, Int<8>{});
+            else vectors(shift, Int<kBatch>{});
+        } else {
+            // Rows that start within a word take more words than windows: 32768 tokens of width 301
+            // 118 us against 68 us; of width 300 58 us against 63 us (777 of 1030 4.2 us against 5.7 us).
+            if constexpr (sizeof(E) == 2) {
+                if (row % 4) return vectors(shift, Int<kBatch>{});
+            }
+            const WordTiles tiles(a, row);
+            auto words = [&](auto W) {
+                unpermute_words_kernel<E, decltype(W)::value><<<tiles.grid, kThreads, 0, stream>>>(
+                    y, a.inv, w, sh, a.T, a.K, even(kBatch), row, tiles.div, to, a.status);
+            };
+            if (tiles.four) words(Int<4>{});
+            else words(Int<1>{});
+        }
     });
     return cudaGetLastError();
 }

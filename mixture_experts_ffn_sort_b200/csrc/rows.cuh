@@ -139,15 +139,18 @@ struct RowWords {
         left = total - (at - lead);
     }
     __device__ __forceinline__ int count() const { return (row_bytes + lead + 3) >> 2; }
-    // Word k, 0 outside of 0 .. count(); its halves that belong to other rows are those rows'.
+    // Word k (outside of 0 .. count(): the nearest); its halves that belong to
+    // other rows are those rows'.
     __device__ __forceinline__ uint32_t word(int k) const {
-        if (k < 0 || k >= count()) return 0;
-        if (!HALF || 4L * k + 4 <= left) return __ldg(reinterpret_cast<const uint32_t*>(base) + k);
-        return __ldg(reinterpret_cast<const uint16_t*>(base) + 2 * k);  // the tensor's last element
+        k = min(max(k, 0), count() - 1);
+        // The tensor's last word may be half a word.
+        return !HALF || 4L * k + 4 <= left ? __ldg(reinterpret_cast<const uint32_t*>(base) + k)
+                                           : __ldg(reinterpret_cast<const uint16_t*>(base) + 2 * k);
     }
-    // Word k (given) as it is for a row of the other start.
-    __device__ __forceinline__ uint32_t shifted(int k, uint32_t same) const {
-        return lead ? __funnelshift_r(same, word(k + 1), 16) : __funnelshift_r(word(k - 1), same, 16);
+    // Word k of a row of the other start, out of word k and beside(k).
+    __device__ __forceinline__ uint32_t beside(int k) const { return word(lead ? k + 1 : k - 1); }
+    __device__ __forceinline__ uint32_t shifted(uint32_t same, uint32_t next) const {
+        return lead ? __funnelshift_r(same, next, 16) : __funnelshift_r(next, same, 16);
     }
 };
 
@@ -163,6 +166,32 @@ __device__ __forceinline__ void store_word(char* tensor, long at, long row_bytes
         if (from >= 0 && from + 2 <= bytes) *reinterpret_cast<uint16_t*>(o) = static_cast<uint16_t>(v);
         if (from == -2) *reinterpret_cast<uint16_t*>(o + 2) = static_cast<uint16_t>(v >> 16);
     }
+}
+
+// A word's elements (f32: one, the second is 0).
+template <class E>
+__device__ __forceinline__ void unpack_word(uint32_t v, float (&f)[2]) {
+    if constexpr (sizeof(E) == 4) {
+        f[0] = __uint_as_float(v);
+        f[1] = 0.f;
+    } else {
+        E e[2];
+        memcpy(e, &v, 4);
+        f[0] = elem_to_float(e[0]);
+        f[1] = elem_to_float(e[1]);
+    }
+}
+__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], __nv_bfloat16) { return pack_bf16x2(f[0], f[1]); }
+__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], __half) {
+    const __half2 h = __floats2half2_rn(f[0], f[1]);
+    uint32_t v;
+    memcpy(&v, &h, 4);
+    return v;
+}
+__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], float) { return __float_as_uint(f[0]); }
+template <class E>
+__device__ __forceinline__ uint32_t pack_word(const float (&f)[2]) {
+    return pack_word_as(f, E{});
 }
 
 // The words at + 128 k (k = 0..3) of shared memory at any 2-byte place `at` of
