@@ -512,9 +512,10 @@ MOE_API int moe_combine(const uint16_t* y_sorted, const int32_t* inv_route, cons
  *              is expert_offsets[E] (pass expert_offsets + E).  The sorted
  *              rows written by the call (x_sorted, dy_sorted) from n_rows on
  *              are then set to zero; with NULL they are left as they were
- *   status     optional device int32, as moe_combine
- * Outputs must not overlap inputs (MOE_ERR_INVALID_ARG).  Results do not
- * depend on the launch: every sum has a fixed order.
+ *   status     optional device int32, as moe_combine; moe_unpermute of long rows
+ *              may also set MOE_STATUS_TIMEOUT (never expected)
+ * Outputs must not overlap inputs (MOE_ERR_INVALID_ARG).  The order of every
+ * sum follows from the sizes and the positions: the same call gives the same bits.
  * Limits: 0 <= T <= MOE_MAX_T, 1 <= K <= MOE_MAX_K, 1 <= H <= MOE_ROWS_MAX_H.
  * ------------------------------------------------------------------------- */
 #define MOE_DTYPE_BF16 0

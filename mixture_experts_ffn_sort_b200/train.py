@@ -41,11 +41,18 @@ class RoutePlan:
     E: int
 
 
+def _base(t: torch.Tensor) -> torch.Tensor:
+    """t as the library takes it: contiguous from a 16-byte boundary on (a slice of a
+    larger tensor, such as the gradient of a concatenation, may start anywhere)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def sort_plan(topk_ids: torch.Tensor, E: int, status: Optional[torch.Tensor] = None) -> RoutePlan:
     """Sort the choices topk_ids [T, K] i32 by expert (an id outside [0, E) is a
     dropped route: it has no row)."""
     T, K = topk_ids.shape
-    off, srt, inv = moe_sort(topk_ids.contiguous(), E, status)
+    off, srt, inv = moe_sort(_base(topk_ids), E, status)
     return RoutePlan(off, srt, inv, T, K, E)
 
 
@@ -62,7 +69,7 @@ class _Route(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, _, dw):
         logits, ids, zero_mask = ctx.saved_tensors
-        return moe_route_bwd(logits, ids, dw.contiguous(), zero_mask=zero_mask, **ctx.cfg), None, None, None
+        return moe_route_bwd(logits, ids, _base(dw), zero_mask=zero_mask, **ctx.cfg), None, None, None
 
 
 def route(logits: torch.Tensor, K: int, score: int = MOE_SCORE_SOFTMAX, sel_bias: Optional[torch.Tensor] = None,
@@ -71,7 +78,7 @@ def route(logits: torch.Tensor, K: int, score: int = MOE_SCORE_SOFTMAX, sel_bias
     """moe_route_ex with a gradient: logits [T, E] f32 -> (topk_ids, topk_w)."""
     cfg = dict(score=score, sel_bias=sel_bias, n_group=n_group, topk_group=topk_group, renormalize=renormalize,
                scaling=scaling)
-    return _Route.apply(logits.contiguous(), K, _mask(zero_mask), cfg)
+    return _Route.apply(_base(logits), K, _mask(zero_mask), cfg)
 
 
 def _mask(zero_mask):
@@ -95,7 +102,7 @@ class _Router(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, _, dw):
         x, w_router, logits, ids, zero_mask = ctx.saved_tensors
-        dlogits = moe_route_bwd(logits, ids, dw.contiguous(), zero_mask=zero_mask, **ctx.cfg)
+        dlogits = moe_route_bwd(logits, ids, _base(dw), zero_mask=zero_mask, **ctx.cfg)
         # The gate GEMM's own gradients: two plain products, in fp32 like its logits.
         dx = (dlogits @ w_router.float()).to(x.dtype) if ctx.needs_input_grad[0] else None
         dwr = (dlogits.t() @ x.float()).to(w_router.dtype) if ctx.needs_input_grad[1] else None
@@ -108,7 +115,7 @@ def router(x: torch.Tensor, w_router: torch.Tensor, K: int, score: int = MOE_SCO
     """moe_router with gradients: x [T, H] bf16 and w_router [E, H] bf16 -> (topk_ids, topk_w)."""
     cfg = dict(score=score, sel_bias=sel_bias, n_group=n_group, topk_group=topk_group, renormalize=renormalize,
                scaling=scaling)
-    return _Router.apply(x.contiguous(), w_router.contiguous(), K, _mask(zero_mask), cfg)
+    return _Router.apply(_base(x), _base(w_router), K, _mask(zero_mask), cfg)
 
 
 class _Permute(torch.autograd.Function):
@@ -122,12 +129,12 @@ class _Permute(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dx_sorted):
         (inv_route,) = ctx.saved_tensors
-        return moe_permute_bwd(dx_sorted.contiguous(), inv_route, ctx.T), None, None
+        return moe_permute_bwd(_base(dx_sorted), inv_route, ctx.T), None, None
 
 
 def permute(x: torch.Tensor, plan: RoutePlan) -> torch.Tensor:
     """Token rows [T, H] -> rows sorted by expert [T*K, H] (zeros behind the last one)."""
-    return _Permute.apply(x.contiguous(), plan.inv_route, plan.expert_offsets)
+    return _Permute.apply(_base(x), plan.inv_route, plan.expert_offsets)
 
 
 class _Unpermute(torch.autograd.Function):
@@ -142,15 +149,14 @@ class _Unpermute(torch.autograd.Function):
     def backward(ctx, dout):
         y_sorted, topk_w, inv_route, expert_offsets = ctx.saved_tensors
         need_dy, need_dw, need_shared = ctx.needs_input_grad[:3]
-        dy, dw = moe_unpermute_bwd(dout.contiguous(), y_sorted, inv_route, topk_w, expert_offsets, need_dy, need_dw)
+        dy, dw = moe_unpermute_bwd(_base(dout), y_sorted, inv_route, topk_w, expert_offsets, need_dy, need_dw)
         return dy, dw, dout if need_shared else None, None, None
 
 
 def unpermute(y_sorted: torch.Tensor, topk_w: torch.Tensor, plan: RoutePlan,
               y_shared: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Sorted rows [T*K, H] and route weights [T, K] (and the shared expert's rows [T, H]) -> [T, H]."""
-    return _Unpermute.apply(y_sorted.contiguous(), topk_w.contiguous(),
-                            None if y_shared is None else y_shared.contiguous(), plan.inv_route, plan.expert_offsets)
+    return _Unpermute.apply(_base(y_sorted), _base(topk_w), None if y_shared is None else _base(y_shared), plan.inv_route, plan.expert_offsets)
 
 
 class RoutedLayer(torch.nn.Module):

@@ -133,6 +133,37 @@ def test_dropped_routes_give_zero_rows_and_no_gradient():
     assert torch.isfinite(g).all()
 
 
+def test_slices_and_gradients_that_start_anywhere():
+    """Rows of 6 bytes out of the middle of larger tensors, gradients of a concatenation."""
+    T, H, K, E = 21, 3, 2, 4
+    _, off, inv = ref.routes(T, K, E, 0.2, 5)
+    plan = train.RoutePlan(off.cuda(), None, inv.cuda(), T, K, E)
+    big = torch.randn((T * K + 9, H), device="cuda").half()
+    wide = torch.rand((T + 3, K), device="cuda")
+    x, y, w, sh = big[1:T + 1], big[5:T * K + 5], wide[1:T + 1], big[3:T + 3]
+    args = [t.clone().requires_grad_() for t in (x, y, w, sh)]
+    sliced = [t.detach().requires_grad_() for t in (x, y, w, sh)]
+    head = torch.randn((5, H), device="cuda").half()
+    grads = []
+    for a, b, c, d in (args, sliced):
+        xs, out = train.permute(a, plan), train.unpermute(b, c, plan, d)
+        loss = (torch.cat([head, xs]).float().square().sum() + torch.cat([head, out]).float().square().sum())
+        grads.append(torch.autograd.grad(loss, (a, b, c, d)))
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+    lg = torch.randn((T + 2, E + 1), device="cuda")
+    ids, rw = train.route(lg[1:T + 1, 1:].requires_grad_(), K)
+    i2, r2 = moe.moe_route(lg[1:T + 1, 1:].clone(), K)
+    assert torch.equal(ids, i2) and torch.equal(rw, r2)
+
+
+def test_no_tokens():
+    layer = train.RoutedLayer(64, 8, 2, Experts(8, 64, torch.bfloat16, 1))
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    out = layer(x)
+    out.sum().backward()
+    assert out.shape == (0, 64) and x.grad.shape == (0, 64) and (layer.w_router.grad == 0).all()
+
+
 def test_forward_and_backward_in_a_graph():
     """One captured step (no eager graph of the same leaves is alive), replayed on new rows."""
     T, H, E, K = 64, 128, 8, 2
