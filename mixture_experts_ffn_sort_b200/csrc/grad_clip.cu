@@ -9,6 +9,7 @@
 // 16-byte vector, then in fp64 per thread, per block (a partial sum in the
 // workspace) and over the partials, always in the same order.
 #include "launch.h"
+#include "launch_after.cuh"
 #include "rows.cuh"
 
 namespace moe {
@@ -137,6 +138,7 @@ template <int CAP, int U>
 __global__ void __launch_bounds__(kThreads, kPerSm) sumsq_kernel(const __grid_constant__ GradTable<CAP> tab,
                                                          double* __restrict__ partial) {
     __shared__ double sh[kThreads / 32];
+    grid_dependency_wait();
     double acc = 0.;
     const int chunks = tab.first[tab.n];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -161,7 +163,7 @@ __device__ __forceinline__ double sum_partials(const double* __restrict__ partia
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restrict__ partial, int n,
                                                           double* __restrict__ sumsq, float* __restrict__ norm) {
     __shared__ double sh[kThreads / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums (see launch_after)
+    grid_dependency_wait();  // the partial sums
     const double s = sum_partials(partial, n, sh);
     if (threadIdx.x == 0) {
         if (sumsq) *sumsq = s;
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
                                                          const double* __restrict__ sumsq, float max_norm, float eps,
                                                          float* __restrict__ norm_out) {
     __shared__ double sh[kThreads / 32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums (see launch_after)
+    grid_dependency_wait();  // the partial sums
     const double s = sumsq ? *sumsq : sum_partials(partial, n_partial, sh);
     const double norm = sqrt(s);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
@@ -289,9 +291,8 @@ cudaError_t launch_partials_of(const moe_tensor_ref* refs, int n, double* partia
     *n_partial = 0;
     for (int at = 0; fill(&tab, refs, n, &at, kChunk<U>);) {
         const int grid = grid_of(tab.first[tab.n]);
-        sumsq_kernel<CAP, U><<<grid, kThreads, 0, stream>>>(tab, partial + *n_partial);
+        cudaError_t e = launch_after(sumsq_kernel<CAP, U>, grid, kThreads, 0, stream, tab, partial + *n_partial);
         *n_partial += grid;
-        cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -304,23 +305,6 @@ cudaError_t launch_partials(const moe_tensor_ref* refs, int n, bool large, doubl
                  : launch_partials_of<CAP, 4>(refs, n, partial, n_partial, stream);
 }
 
-// Launches a kernel as a programmatic dependent of the one before it, so that
-// its blocks are in place when that one is done; it waits for all of that
-// kernel (griddepcontrol.wait) before it reads or writes anything.
-template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), int grid, cudaStream_t stream, const A&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <int CAP>
 cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps, float* norm,
                         double* partial, cudaStream_t stream) {
@@ -330,7 +314,7 @@ cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, 
         cudaError_t e = launch_partials<CAP>(refs, n, large, partial, &np, stream);
         if (e == cudaSuccess && large) {  // one block adds the partial sums for all
             double* total = partial + np;
-            e = launch_after(finish_kernel, 1, stream, partial, np, total, norm);
+            e = launch_after(finish_kernel, 1, kThreads, 0, stream, partial, np, total, norm);
             sumsq = total;
             norm = nullptr;
         }
@@ -340,12 +324,13 @@ cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, 
     bool any = false;
     for (int at = 0; fill(&tab, refs, n, &at, kChunk<kScaleU>); any = true) {
         const int chunks = tab.first[tab.n];
-        cudaError_t e = launch_after(scale_kernel<CAP>, large ? chunks : grid_of(chunks), stream, tab, partial, np,
-                                     sumsq, max_norm, eps, any ? static_cast<float*>(nullptr) : norm);
+        cudaError_t e = launch_after(scale_kernel<CAP>, large ? chunks : grid_of(chunks), kThreads, 0, stream, tab,
+                                     partial, np, sumsq, max_norm, eps, any ? static_cast<float*>(nullptr) : norm);
         if (e != cudaSuccess) return e;
     }
     // No values: the norm alone.
-    if (!any && norm) return launch_after(scale_kernel<CAP>, 1, stream, tab, partial, np, sumsq, max_norm, eps, norm);
+    if (!any && norm)
+        return launch_after(scale_kernel<CAP>, 1, kThreads, 0, stream, tab, partial, np, sumsq, max_norm, eps, norm);
     return cudaSuccess;
 }
 
@@ -371,7 +356,7 @@ cudaError_t launch_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, 
     const bool large = is_large(refs, n);
     cudaError_t e = n <= kFew ? launch_partials<kFew>(refs, n, large, partial, &np, stream)
                               : launch_partials<kCap>(refs, n, large, partial, &np, stream);
-    return e != cudaSuccess ? e : launch_after(finish_kernel, 1, stream, partial, np, sumsq, norm);
+    return e != cudaSuccess ? e : launch_after(finish_kernel, 1, kThreads, 0, stream, partial, np, sumsq, norm);
 }
 
 cudaError_t launch_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps,

@@ -9,6 +9,7 @@
 // warp's tokens are written as zeros (or as the unchosen experts' softmax
 // term) and the K chosen gradients are stored over them.
 #include "launch.h"
+#include "launch_after.cuh"
 #include "route_device.cuh"
 
 namespace moe {
@@ -48,6 +49,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
                                                         float* __restrict__ dlogits, int32_t* __restrict__ status) {
     constexpr int TPW = 32 / G;  // tokens of a warp
     const int t0 = ((blockIdx.x * blockDim.x + threadIdx.x) >> 5) * TPW;
+    grid_dependency_wait();
     if (t0 >= T) return;
     const int lane = threadIdx.x & 31, j = lane % G;
     const int t = t0 + lane / G;
@@ -114,24 +116,25 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
 cudaError_t launch_route_bwd(const float* logits, const int32_t* ids, const float* dw, int T, int E, int K,
                              const RouteCfg& cfg, const uint8_t* zero_mask, float* dlogits, int32_t* status,
                              cudaStream_t stream) {
-#define MOE_LAUNCH(S, N, G)                                                                                   \
-    route_bwd_kernel<S, N, G><<<(T + 8 * (32 / G) - 1) / (8 * (32 / G)), 256, 0, stream>>>(                   \
-        logits, ids, dw, T, E, K, cfg.scaling, zero_mask, dlogits, status)
-#define MOE_LAUNCH_G(S, N)             \
-    if (K <= 8) MOE_LAUNCH(S, N, 8);   \
-    else if (K <= 16) MOE_LAUNCH(S, N, 16); \
-    else MOE_LAUNCH(S, N, 32);
+    auto launch = [&](auto kernel, int G) {
+        const int tokens = 8 * (32 / G);  // of a block
+        return launch_after(kernel, (T + tokens - 1) / tokens, 256, 0, stream, logits, ids, dw, T, E, K, cfg.scaling,
+                            zero_mask, dlogits, status);
+    };
     if (cfg.score == MOE_SCORE_SOFTMAX) {
         // The full softmax reads and writes whole rows: a warp for each.
-        if (!cfg.renormalize) MOE_LAUNCH(true, false, 32);
-        else { MOE_LAUNCH_G(true, true) }
-    } else {
-        if (cfg.renormalize) { MOE_LAUNCH_G(false, true) }
-        else { MOE_LAUNCH_G(false, false) }
+        if (!cfg.renormalize) return launch(route_bwd_kernel<true, false, 32>, 32);
+        return K <= 8 ? launch(route_bwd_kernel<true, true, 8>, 8)
+                      : K <= 16 ? launch(route_bwd_kernel<true, true, 16>, 16)
+                                : launch(route_bwd_kernel<true, true, 32>, 32);
     }
-#undef MOE_LAUNCH_G
-#undef MOE_LAUNCH
-    return cudaGetLastError();
+    if (cfg.renormalize)
+        return K <= 8 ? launch(route_bwd_kernel<false, true, 8>, 8)
+                      : K <= 16 ? launch(route_bwd_kernel<false, true, 16>, 16)
+                                : launch(route_bwd_kernel<false, true, 32>, 32);
+    return K <= 8 ? launch(route_bwd_kernel<false, false, 8>, 8)
+                  : K <= 16 ? launch(route_bwd_kernel<false, false, 16>, 16)
+                            : launch(route_bwd_kernel<false, false, 32>, 32);
 }
 
 }  // namespace moe

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "launch.h"
+#include "launch_after.cuh"
 #include "rows.cuh"
 
 namespace moe {
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const char* __restric
                                                            char* __restrict__ x_sorted, int32_t* __restrict__ status) {
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * vecs.d;
     bool bad = false;
+    grid_dependency_wait();
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long>(gridDim.x) * blockDim.x) {
         const long t = vecs.div(i), c = i - t * vecs.d;
@@ -87,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) permute_words_kernel(const char* __r
                                                                  int32_t* __restrict__ status) {
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * tiles.d * (W > 1 ? 32 : 1);
     bool bad = false;
+    grid_dependency_wait();
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long>(gridDim.x) * blockDim.x) {
         const long tile = W > 1 ? i >> 5 : i, t = tiles.div(tile);
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
     constexpr int N = kVec<E>;
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * vecs.d;
     bool bad = false;
+    grid_dependency_wait();
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long>(gridDim.x) * blockDim.x) {
         const long t = vecs.div(i), c = i - t * vecs.d;
@@ -198,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* _
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * tiles.d * (W > 1 ? 32 : 1);
     const int words = static_cast<int>(row_bytes >> 2);
     bool bad = false;
+    grid_dependency_wait();
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long>(gridDim.x) * blockDim.x) {
         const long tile = W > 1 ? i >> 5 : i, t = tiles.div(tile);
@@ -408,6 +413,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) unpermute_ring_kernel(const R
         fence_proxy_async_smem();
     }
     __syncthreads();
+    grid_dependency_wait();
     // The items of this team: every step-th from the first.
     const long first_item = static_cast<long>(blockIdx.x) * kTeams + team;
     const long step = static_cast<long>(gridDim.x) * kTeams;
@@ -528,6 +534,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(
     const long R = static_cast<long>(T) * K.d;
     const int lane = threadIdx.x % G, vecs = static_cast<int>(row_bytes >> 4);
     bool bad = false;
+    grid_dependency_wait();
     for (long r0 = static_cast<long>(blockIdx.x) * (PER * RU); r0 < R; r0 += static_cast<long>(gridDim.x) * (PER * RU)) {
         int32_t p[RU];
         float wr[RU], dot[RU];
@@ -603,6 +610,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_bwd_shift_kernel(
     const long R = static_cast<long>(T) * K.d;
     const int lane = threadIdx.x % G, bytes = static_cast<int>(row_bytes);
     bool bad = false;
+    grid_dependency_wait();
     for (long r0 = static_cast<long>(blockIdx.x) * PER; r0 < R; r0 += static_cast<long>(gridDim.x) * PER) {
         const long r = r0 + threadIdx.x / G;
         const int32_t p = r < R ? position(inv, r, R, &bad) : -1;
@@ -713,18 +721,16 @@ cudaError_t launch_permute(const RowsArgs& a, const void* x, void* x_sorted, cud
     char* out = static_cast<char*>(x_sorted);
     if (row % 16 == 0) {
         const FastDiv vecs(static_cast<unsigned>(row / 16));
-        permute_kernel<<<grid_for(static_cast<long>(a.T) * vecs.d), kThreads, 0, stream>>>(
-            in, a.inv, a.n_rows, a.T, a.K, row, vecs, out, a.status);
-        return cudaGetLastError();
+        return launch_after(permute_kernel, grid_for(static_cast<long>(a.T) * vecs.d), kThreads, 0, stream, in, a.inv, a.n_rows, a.T, a.K,
+                            row, vecs, out, a.status);
     }
     const WordTiles tiles(a, row);
     auto launch = [&](auto half, auto w) {
-        permute_words_kernel<decltype(half)::value, decltype(w)::value><<<tiles.grid, kThreads, 0, stream>>>(
-            in, a.inv, a.n_rows, a.T, a.K, row, tiles.div, out, a.status);
+        return launch_after(permute_words_kernel<decltype(half)::value, decltype(w)::value>, tiles.grid, kThreads, 0,
+                            stream, in, a.inv, a.n_rows, a.T, a.K, row, tiles.div, out, a.status);
     };
-    if (row % 4) tiles.four ? launch(std::true_type{}, Int<4>{}) : launch(std::true_type{}, Int<1>{});
-    else tiles.four ? launch(std::false_type{}, Int<4>{}) : launch(std::false_type{}, Int<1>{});
-    return cudaGetLastError();
+    if (row % 4) return tiles.four ? launch(std::true_type{}, Int<4>{}) : launch(std::true_type{}, Int<1>{});
+    return tiles.four ? launch(std::false_type{}, Int<4>{}) : launch(std::false_type{}, Int<1>{});
 }
 
 namespace {
@@ -760,8 +766,7 @@ cudaError_t launch_unpermute_ring(const RowsArgs& a, const void* y_sorted, const
         static_assert(smem <= 227 * 1024, "the rings exceed an SM's shared memory");
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return;
-        kernel<<<static_cast<int>(blocks < sms ? blocks : sms), kRingThreads, smem, stream>>>(g);
-        e = cudaGetLastError();
+        e = launch_after(kernel, static_cast<int>(blocks < sms ? blocks : sms), kRingThreads, smem, stream, g);
     });
     return e;
 }
@@ -775,6 +780,7 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* y_sorted, const floa
         return launch_unpermute_ring(a, y_sorted, w, y_shared, out, stream);
     const char *y = static_cast<const char*>(y_sorted), *sh = static_cast<const char*>(y_shared);
     char* to = static_cast<char*>(out);
+    cudaError_t err = cudaSuccess;
     auto even = [&](int most) { return (a.K + (a.K + most - 1) / most - 1) / ((a.K + most - 1) / most); };
     dispatch(a, [&](auto e, auto shift) {
         using E = decltype(e);
@@ -782,8 +788,8 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* y_sorted, const floa
         const int grid = grid_for(static_cast<long>(a.T) * vecs.d);
         auto vectors = [&](auto sh_, auto most) {
             constexpr int B = decltype(most)::value;
-            unpermute_kernel<E, decltype(sh_)::value, B><<<grid, kThreads, 0, stream>>>(y, a.inv, w, sh, a.T, a.K,
-                                                                                      even(B), row, vecs, to, a.status);
+            err = launch_after(unpermute_kernel<E, decltype(sh_)::value, B>, grid, kThreads, 0, stream, y, a.inv, w, sh,
+                               a.T, a.K, even(B), row, vecs, to, a.status);
         };
         if constexpr (!decltype(shift)::value) {
             // One wave of blocks: one batch of all slots is one wait less (64 tokens of width 2048,
@@ -799,14 +805,14 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* y_sorted, const floa
             }
             const WordTiles tiles(a, row);
             auto words = [&](auto W) {
-                unpermute_words_kernel<E, decltype(W)::value><<<tiles.grid, kThreads, 0, stream>>>(
-                    y, a.inv, w, sh, a.T, a.K, even(kBatch), row, tiles.div, to, a.status);
+                err = launch_after(unpermute_words_kernel<E, decltype(W)::value>, tiles.grid, kThreads, 0, stream, y,
+                                   a.inv, w, sh, a.T, a.K, even(kBatch), row, tiles.div, to, a.status);
             };
             if (tiles.four) words(Int<4>{});
             else words(Int<1>{});
         }
     });
-    return cudaGetLastError();
+    return err;
 }
 
 cudaError_t launch_unpermute_bwd(const RowsArgs& a, const void* dout, const void* y_sorted, const float* w,
@@ -819,14 +825,15 @@ cudaError_t launch_unpermute_bwd(const RowsArgs& a, const void* dout, const void
     const int g = vecs > 64 && R < 148 * 16 ? 256 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
     const char *d = static_cast<const char*>(dout), *y = static_cast<const char*>(y_sorted);
     char* dy = static_cast<char*>(dy_sorted);
+    cudaError_t err = cudaSuccess;
     dispatch(a, [&](auto e, auto shift) {
         using E = decltype(e);
         if constexpr (!decltype(shift)::value) {
             auto launch = [&](auto G, auto RU, auto U) {
                 constexpr int kG = decltype(G)::value, kRU = decltype(RU)::value;
-                unpermute_bwd_kernel<E, kG, kRU, decltype(U)::value>
-                    <<<grid_for((R + kRU - 1) / kRU * kG), kThreads, 0, stream>>>(d, y, a.inv, w, a.n_rows, a.T, K,
-                                                                                 row, dy, dw, a.status);
+                err = launch_after(unpermute_bwd_kernel<E, kG, kRU, decltype(U)::value>,
+                                   grid_for((R + kRU - 1) / kRU * kG), kThreads, 0, stream, d, y, a.inv, w, a.n_rows,
+                                   a.T, K, row, dy, dw, a.status);
             };
             if (vecs <= 8) launch(Int<8>{}, Int<2>{}, Int<1>{});
             else if (g == 8) launch(Int<8>{}, Int<1>{}, Int<4>{});
@@ -836,8 +843,8 @@ cudaError_t launch_unpermute_bwd(const RowsArgs& a, const void* dout, const void
         } else {
             auto launch = [&](auto G) {
                 constexpr int kG = decltype(G)::value;
-                unpermute_bwd_shift_kernel<E, kG><<<grid_for(R * kG), kThreads, 0, stream>>>(
-                    d, y, a.inv, w, a.n_rows, a.T, K, row, dy, dw, a.status);
+                err = launch_after(unpermute_bwd_shift_kernel<E, kG>, grid_for(R * kG), kThreads, 0, stream, d, y,
+                                   a.inv, w, a.n_rows, a.T, K, row, dy, dw, a.status);
             };
             if (g == 8) launch(Int<8>{});
             else if (g == 16) launch(Int<16>{});
@@ -845,7 +852,7 @@ cudaError_t launch_unpermute_bwd(const RowsArgs& a, const void* dout, const void
             else launch(Int<256>{});
         }
     });
-    return cudaGetLastError();
+    return err;
 }
 
 }  // namespace moe
