@@ -8,6 +8,10 @@
 // all chunks of the launch.  Values are squared and added in fp32 over one
 // 16-byte vector, then in fp64 per thread, per block (a partial sum in the
 // workspace) and over the partials, always in the same order.
+//
+// Bound by memory: 769 bf16 tensors of 2 MB are summed in 246 us, 6.6 TB/s, and
+// scaled into other memory in 511 us, 6.3 TB/s.  The norm has to be known before
+// anything is scaled, so what does not fit L2 is read twice.
 #include "launch.h"
 #include "launch_after.cuh"
 #include "rows.cuh"

@@ -1,13 +1,19 @@
 // route_bwd.cu -- the gradient of the routing (moe_route_bwd): from the K
 // route weights of a token to its E logits, the choice held fixed.
 //
-// G lanes per token (8, 16 or 32, at least K), lane j holding choice j.  The K
+// G lanes per token (8, 16 or 32, at least K), lane j holding choice j, so that
+// a warp has the loads of several tokens in flight.  The K
 // scores are recomputed from the K chosen logits (softmax relative to the
 // largest of them, which cancels; the full normaliser, when the weights are
 // not renormalised, needs the whole row), then dl_j = scaling * q_j *
 // (G_j - sum_i G_i q_i), times (1 - s_j) for sigmoid scores.  The rows of a
 // warp's tokens are written as zeros (or as the unchosen experts' softmax
-// term) and the K chosen gradients are stored over them.
+// term) and the K chosen gradients are stored over them, after the loads: zeros
+// that go first delay them (21.5 us against 19.1 us with a warp a token).
+//
+// 32768 tokens of 512 experts, top-10, sigmoid: 16.4 us, 6.2 TB/s of 67 MB
+// written and 35 MB read, since each of the ten scattered logits of a row
+// brings its whole piece of DRAM.
 #include "launch.h"
 #include "launch_after.cuh"
 #include "route_device.cuh"

@@ -53,7 +53,8 @@ __device__ __forceinline__ void zero_tail(const int32_t* __restrict__ n_rows, lo
 }
 
 // x_sorted[inv[t, j]] = x[t].  One thread per 16-byte column of a token: one
-// load, K stores.
+// load, K stores.  Bound by the writes: 8192 bf16 rows of 4096, top-10, in 121
+// us, 6.1 TB/s of the 738 MB it cannot do without.
 __global__ void __launch_bounds__(kThreads) permute_kernel(const char* __restrict__ x,
                                                            const int32_t* __restrict__ inv,
                                                            const int32_t* __restrict__ n_rows, int T, int K,
@@ -140,7 +141,9 @@ __device__ __forceinline__ void slot_batch(const int32_t* __restrict__ inv, cons
 // out[t] = sum_j w[t, j] y[inv[t, j]] (+ y_shared[t]).  One thread per 16-byte
 // column of a token; slots in batches: all positions, then all rows, then the
 // sums in slot order, so that the loads of a batch (of at most B) are in flight
-// together.  SHIFT: rows that start anywhere, by shifted windows.
+// together.  SHIFT: rows that start anywhere, by shifted windows.  8192 bf16
+// rows of 4096, top-10: 135 us, which the ring below takes to 113 us; here are
+// the calls that are too small for it, bound by latency.
 template <class E, bool SHIFT, int B>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restrict__ y_sorted,
                                                              const int32_t* __restrict__ inv,
@@ -271,6 +274,10 @@ __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* _
 // Rows that are no multiple of 16 bytes start anywhere in their slots: there a
 // thread takes every 32nd 4-byte word of its warp's 512 bytes, which needs no
 // shift unless the row starts within a word, and no bank twice.
+//
+// 8192 bf16 rows of 4096, top-10: 111 us, 6.6 TB/s of 739 MB, with 73 % of the
+// issue slots in use (two teams 118 us, one 155 us: the sums of 16-bit rows
+// need the warps); of 4095: 131 us, bound by instructions.
 
 constexpr int kConsumers = 8;  // warps of a team
 constexpr int kTeams = 3;
@@ -284,7 +291,9 @@ constexpr int kShiftPad = 64;
 static_assert(kConsumers * kGroup <= 32, "a lane for every row of a stage");
 static_assert(kRingBytes / (kConsumers * kGroup * (512 + kShiftPad)) >= kProducers, "the ring has too few stages");
 // Taken for rows of at least kRingMinRow bytes and sorted rows of so many bytes
-// in all, where it overtakes the plain kernel, which starts faster.
+// in all, where it overtakes the plain kernel, which starts faster: 42 MB 14.1
+// us against 11.9 us, 84 MB 20.3 us against 21.5 us; rows of 4095 elements 42 MB
+// 16.5 us against 20.1 us; rows of 512 bytes 33.2 us against 31.6 us (134 MB).
 constexpr long kRingMinRow = 1024;
 constexpr long kRingMinBytes = 64L << 20, kRingMinBytesShift = 24L << 20;
 
@@ -295,7 +304,7 @@ struct RingMeta {
 
 struct RingHead {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    RingMeta meta[kMaxStages][kConsumers * kGroup];
+    RingMeta meta[kMaxStages][32];  // a producer's lane for every row
 };
 constexpr int kRingHead = (sizeof(RingHead) * kTeams + 16 + 127) / 128 * 128;
 
@@ -446,54 +455,50 @@ __global__ void __launch_bounds__(kRingThreads, 1) unpermute_ring_kernel(const R
     } else {
         // A thread's columns: 16 bytes of its warp's 512, or with SHIFT every 32nd 4-byte word of them.
         const int own = warp % kConsumers, sub = own / a.m, col = (own % a.m) * 512 + lane * (SHIFT ? 4 : 16);
-        long item = first_item;
-        int group = 0, stage = 0;
+        int stage = 0;
         uint32_t parity = 0;
-        float acc[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) acc[n] = 0.f;
-        for (long s = 0; s < steps; ++s) {
-            const bool ok = mbar_wait_or_abort(&head->full[stage], parity, abort_flag, a.status);
-            if (!__all_sync(0xffffffffu, ok)) break;
+        bool ok = true;
+        for (long item = first_item; ok && item < a.items; item += step) {
             const long tb = a.pieces.div(item), t = tb * a.tokens + sub;
             const Piece piece = Piece::of<SHIFT>(a, t, item - tb * a.pieces.d);
             const long rel = piece.begin + col;  // this thread's first column of the output row
             const bool here = t < a.T && rel < a.row_bytes;
-            if (here) {
-                const RingMeta* meta = head->meta[stage] + sub * a.group;
-                const char* slot = slots + (stage * a.tokens + sub) * (a.group * a.slot);
-                const int at = SHIFT ? static_cast<int>(piece.begin - piece.from) + col : col;
-                RingMeta mt[kGroup];
-                uint4 v[kGroup];
+            const int at = SHIFT ? static_cast<int>(piece.begin - piece.from) + col : col;
+            float acc[N];
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g) {
-                    mt[g].at = -1;
-                    if (g < a.group) mt[g] = meta[g];
-                    const char* row = slot + g * a.slot;
-                    if (mt[g].at >= 0)
-                        v[g] = SHIFT ? load_shared_words(row, mt[g].at + at)
-                                     : *reinterpret_cast<const uint4*>(row + at);
-                }
-#pragma unroll
-                for (int g = 0; g < kGroup; ++g)
-                    if (mt[g].at >= 0) add_weighted<E>(acc, v[g], mt[g].w);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&head->empty[stage]);
-            if (++stage == a.stages) {
-                stage = 0;
-                parity ^= 1;
-            }
-            if (++group == a.groups) {
+            for (int n = 0; n < N; ++n) acc[n] = 0.f;
+            for (int group = 0; group < a.groups; ++group) {
+                ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&head->full[stage], parity, abort_flag, a.status));
+                if (!ok) break;
                 if (here) {
-                    char* o = a.out + t * a.row_bytes + rel;
-                    if (SHIFT) store_words<E>(o, pack<E>(acc), rel, a.row_bytes);
-                    else *reinterpret_cast<uint4*>(o) = pack<E>(acc);
-                }
+                    const RingMeta* meta = head->meta[stage] + sub * a.group;
+                    const char* slot = slots + (stage * a.tokens + sub) * (a.group * a.slot);
+                    RingMeta mt[kGroup];
+                    uint4 v[kGroup];
 #pragma unroll
-                for (int n = 0; n < N; ++n) acc[n] = 0.f;
-                group = 0;
-                item += step;
+                    for (int g = 0; g < kGroup; ++g) {
+                        mt[g].at = -1;
+                        if (g < a.group) mt[g] = meta[g];
+                        const char* row = slot + g * a.slot;
+                        if (mt[g].at >= 0)
+                            v[g] = SHIFT ? load_shared_words(row, mt[g].at + at)
+                                         : *reinterpret_cast<const uint4*>(row + at);
+                    }
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g)
+                        if (mt[g].at >= 0) add_weighted<E>(acc, v[g], mt[g].w);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&head->empty[stage]);
+                if (++stage == a.stages) {
+                    stage = 0;
+                    parity ^= 1;
+                }
+            }
+            if (ok && here) {
+                char* o = a.out + t * a.row_bytes + rel;
+                if (SHIFT) store_words<E>(o, pack<E>(acc), rel, a.row_bytes);
+                else *reinterpret_cast<uint4*>(o) = pack<E>(acc);
             }
         }
     }
@@ -522,7 +527,9 @@ __device__ __forceinline__ float lanes_sum(float dot, float* sh) {
 
 // dy[p] = w dout[t], dw = <dout[t], y[p]> for p = inv[t, j].  G threads per
 // route and RU routes at a time, each thread with every G-th 16-byte vector,
-// U of them at a time.
+// U of them at a time.  8192 bf16 rows of 4096, top-10: 215 us, 6.6 TB/s of
+// 1.41 GB (dout's row comes from L1 and L2 for all but the first of its K
+// routes).  Short rows are bound by what a route costs, about 9 ns an SM.
 template <class E, int G, int RU, int U>
 __global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(
     const char* __restrict__ dout, const char* __restrict__ y_sorted, const int32_t* __restrict__ inv,
@@ -597,6 +604,8 @@ __global__ void __launch_bounds__(kThreads) unpermute_bwd_kernel(
 // memory that the sorted row touches, dout's bytes shifted to them (by the same
 // distance for all of a route).  Blocks at least one away from the row's ends
 // need no check of bounds; the first and the last two are taken with care.
+// 8192 bf16 rows of 4095, top-10: 279 us, bound by instructions and latency
+// (four vectors at a time cost more warps than they gain: 334 us).
 template <class E, int G>
 __global__ void __launch_bounds__(kThreads) unpermute_bwd_shift_kernel(
     const char* __restrict__ dout, const char* __restrict__ y_sorted, const int32_t* __restrict__ inv,
@@ -742,14 +751,14 @@ cudaError_t launch_unpermute_ring(const RowsArgs& a, const void* y_sorted, const
     RingArgs g{static_cast<const char*>(y_sorted), a.inv, w, static_cast<const char*>(y_shared),
                static_cast<char*>(out), a.status, a.T, a.K, a.K + (y_shared ? 1 : 0), 0, 0, 8, 1, 0, 0, R, row, 0,
                FastDiv(1)};
-    g.groups = (g.rows + kGroup - 1) / kGroup;
-    g.group = (g.rows + g.groups - 1) / g.groups;
     // Warps of a token: the most whose pieces are filled to 8/9 on average.  (A
     // shifted row's words may begin 2 bytes before it.)
     const long span = row + (a.dtype != MOE_DTYPE_F32 && row % 4 ? 2 : 0);
     auto padded = [&](long m) { return (span + 512 * m - 1) / (512 * m) * (512 * m); };
     while (g.m > 1 && padded(g.m) * 8 > span * 9) g.m /= 2;
     g.tokens = kConsumers / g.m;
+    g.groups = (g.rows + kGroup - 1) / kGroup;
+    g.group = (g.rows + g.groups - 1) / g.groups;
     const long size = g.m * 512;
     g.pieces = FastDiv(static_cast<unsigned>(padded(g.m) / size));
     g.items = (static_cast<long>(a.T) + g.tokens - 1) / g.tokens * g.pieces.d;
@@ -819,9 +828,10 @@ cudaError_t launch_unpermute_bwd(const RowsArgs& a, const void* dout, const void
                                  void* dy_sorted, float* dw, cudaStream_t stream) {
     const long row = row_bytes_of(a), R = static_cast<long>(a.T) * a.K, vecs = (row + 15) / 16;
     const FastDiv K(static_cast<unsigned>(a.K));
-    // Threads per route: so few that each has four vectors (a quarter of the
-    // overhead of a route with one), down to 8, but a whole block while the
-    // routes are too few to fill the GPU with warps.
+    // Threads per route: so few that each has four vectors, down to 8 (32768
+    // tokens of width 256: 58 us with 8, 114 us with 32 threads), but a whole
+    // block while the routes are too few to fill the GPU with warps (64 tokens
+    // of width 7168: 4.1 us against 10.0 us).
     const int g = vecs > 64 && R < 148 * 16 ? 256 : vecs <= 32 ? 8 : vecs <= 64 ? 16 : 32;
     const char *d = static_cast<const char*>(dout), *y = static_cast<const char*>(y_sorted);
     char* dy = static_cast<char*>(dy_sorted);
