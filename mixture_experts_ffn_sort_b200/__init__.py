@@ -454,6 +454,8 @@ def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch
     y_sorted [T*K, H] (bf16, f16 or f32), topk_w [T, K] f32 (and y_shared
     [T, H]) -> out [T, H], summed in fp32.  (moe_combine takes rows that carry
     their weight already.)"""
+    if topk_w is None:
+        raise ValueError("topk_w must be a tensor (moe_permute_bwd adds rows without weights)")
     if stream is not None:
         with _on(stream, y_sorted.device):
             return moe_unpermute(y_sorted, inv_route, topk_w, y_shared, out, status)

@@ -3,11 +3,12 @@
 //
 // The tensors' addresses travel in the kernel's parameters (no copy of a table
 // to the device, so the calls can be captured in a graph), a launch taking up
-// to GradTable::kMax of them.  Every tensor is cut into chunks of 16 KB on
-// 16-byte boundaries of its own memory; a grid of a few blocks per SM walks
-// all chunks of the launch.  Values are squared and added in fp32 over one
-// 16-byte vector, then in fp64 per thread, per block (a partial sum in the
-// workspace) and over the partials, always in the same order.
+// to kCap of them.  Every tensor is cut into chunks on 16-byte boundaries of its
+// own memory.  A grid of a few blocks per SM sums the chunks of a launch; a grid
+// of the same size or, for large lists, a block for every chunk scales them.
+// Values are squared and added in fp32 over one 16-byte vector, then in fp64 per
+// thread, per block (a partial sum in the workspace) and over the partials,
+// always in the same order.
 //
 // Bound by memory: 769 bf16 tensors of 2 MB are summed in 246 us, 6.6 TB/s, and
 // scaled into other memory in 511 us, 6.3 TB/s.  The norm has to be known before
@@ -63,7 +64,8 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
 }
 
 // The squares of one 16-byte vector: in fp32, and in fp64 where fp32 would
-// overflow or lose them.
+// overflow or lose them.  (From 1e-36 on, eight squares that are rounded to
+// multiples of 2^-149 are off by less than 2^-26 of their sum.)
 template <class E>
 __device__ __forceinline__ double vec_sumsq(const uint4& raw) {
     constexpr int N = 16 / sizeof(E);
@@ -72,7 +74,7 @@ __device__ __forceinline__ double vec_sumsq(const uint4& raw) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) s = fmaf(f[i], f[i], s);
-    if ((s > 1e-20f && s < 1e30f) || !(raw.x | raw.y | raw.z | raw.w)) return s;
+    if ((s > 1e-36f && s < 1e30f) || !(raw.x | raw.y | raw.z | raw.w)) return s;
     double d = 0.;
 #pragma unroll
     for (int i = 0; i < N; ++i) d = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), d);

@@ -14,7 +14,9 @@ runs them in order around a function of the sorted rows; clip_grad_norm clips
 its gradients (and any others) by their global norm.
 
 Every function runs on the current stream.  Gradients of gradients are not
-defined.
+defined.  A step may be captured in a CUDA graph after a first one, with
+torch.autograd.grad, or with backward() as long as no eager graph of the same
+leaves is alive.
 """
 from __future__ import annotations
 
