@@ -751,11 +751,12 @@ cudaError_t launch_unpermute_ring(const RowsArgs& a, const void* y_sorted, const
     RingArgs g{static_cast<const char*>(y_sorted), a.inv, w, static_cast<const char*>(y_shared),
                static_cast<char*>(out), a.status, a.T, a.K, a.K + (y_shared ? 1 : 0), 0, 0, 8, 1, 0, 0, R, row, 0,
                FastDiv(1)};
-    // Warps of a token: the most whose pieces are filled to 8/9 on average.  (A
-    // shifted row's words may begin 2 bytes before it.)
+    // Warps of a token: the most whose pieces are filled to 8/9 on average, or as
+    // well as those of any fewer.  (A shifted row's words may begin 2 bytes before it.)
     const long span = row + (a.dtype != MOE_DTYPE_F32 && row % 4 ? 2 : 0);
     auto padded = [&](long m) { return (span + 512 * m - 1) / (512 * m) * (512 * m); };
-    while (g.m > 1 && padded(g.m) * 8 > span * 9) g.m /= 2;
+    for (int m = 8; m > 0 && padded(g.m) * 8 > span * 9; m /= 2)
+        if (padded(m) < padded(g.m)) g.m = m;
     g.tokens = kConsumers / g.m;
     g.groups = (g.rows + kGroup - 1) / kGroup;
     g.group = (g.rows + g.groups - 1) / g.groups;

@@ -207,3 +207,76 @@ def test_sharded_norm_without_a_group():
     assert abs(float(got) - norm) <= 8 * U32 * norm
     for t, q in zip(a + b, before):
         assert ((t.double() - q / norm).abs() <= (HALF[t.dtype] + 30 * U32 + 1e-6 / norm) * q.abs() / norm).all()
+
+
+def test_a_capture_that_forks_and_joins():
+    """The calls on two captured streams, joined, and replayed on new values."""
+    T, H, K, E = 90, 264, 4, 8
+    ids, off, inv = (t.cuda() for t in ref.routes(T, K, E, 0.2, 21))
+    x, y = torch.randn((T, H), device="cuda"), torch.randn((T * K, H), device="cuda")
+    w, lg = torch.rand((T, K), device="cuda"), torch.randn((T, E), device="cuda")
+
+    def left():
+        return [moe.moe_permute(x, inv, off), *moe.moe_unpermute_bwd(x, y, inv, w, off)]
+
+    def right():
+        return [moe.moe_unpermute(y, inv, w), moe.moe_route_bwd(lg, ids, w), moe.moe_grad_norm([x, y])]
+
+    def both():
+        a, b = left(), right()
+        return a + b + [moe.moe_unpermute(a[0], inv, w), a[1] * 2]
+
+    both()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            b = right()
+        a = left()
+        torch.cuda.current_stream().wait_stream(side)
+        cap = a + b + [moe.moe_unpermute(a[0], inv, w), a[1] * 2]
+    for t in (x, y, w, lg):
+        t.copy_(torch.randn_like(t))
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(cap, both()))
+
+
+def test_calls_from_several_threads():
+    """Four host threads, each on a stream of its own, with lists and rows of their own."""
+    import threading
+    T, H, K, E = 64, 520, 4, 8
+    failures = []
+
+    def work(k):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                _, off, inv = (t.cuda() for t in ref.routes(T, K, E, 0.2, 30 + k))
+                x = torch.randn((T, H), generator=ref.gen(k)).cuda()
+                w = torch.rand((T, K), generator=ref.gen(k)).cuda()
+                want = None
+                for _ in range(30):
+                    xs = moe.moe_permute(x, inv, off)
+                    out = moe.moe_unpermute(xs, inv, w)
+                    dy, dw = moe.moe_unpermute_bwd(out, xs, inv, w, off)
+                    got = [xs, out, dy, dw, moe.moe_grad_clip([dy.clone(), dw.clone()], 1.0)]
+                    if want is None:
+                        want = got
+                    elif not all(torch.equal(p, q) for p, q in zip(got, want)):
+                        failures.append(k)
+                try:
+                    moe.moe_permute(x, inv[:-1])
+                    failures.append("accepted")
+                except ValueError:
+                    pass
+        except Exception as e:  # reported below
+            failures.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
