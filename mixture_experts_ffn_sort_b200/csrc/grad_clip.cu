@@ -13,6 +13,8 @@
 // Bound by memory: 769 bf16 tensors of 2 MB are summed in 245 us, 6.6 TB/s, and
 // scaled into other memory in 495 us, 6.5 TB/s.  The norm has to be known before
 // anything is scaled, so what does not fit L2 is read twice.
+#include <type_traits>
+
 #include "launch.h"
 #include "launch_after.cuh"
 #include "rows.cuh"
@@ -37,7 +39,7 @@ struct GradTable {
     int first[CAP + 1];    // first chunk of each tensor; first[n] = chunks in all
     // Where to look for a chunk's tensor: hint[h] holds chunk h << shift, the
     // last one the last chunk.
-    static constexpr int kHints = CAP > 32 ? 1024 : 64;
+    static constexpr int kHints = CAP < 1000 ? 2 * CAP : 1024;
     uint16_t hint[kHints + 1];
     int shift, n;
 };
@@ -251,9 +253,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
 }
 
 // Tensors of a launch: the table is 28 bytes for each, and 2 KB of hints, and a
-// kernel's parameters hold 32,764.  Up to kFew tensors travel in a small table.
+// kernel's parameters hold 32,764.  Every launch copies the whole table, about
+// 3 us on the host for the largest, so there are smaller ones.
 constexpr int kCap = 1000;
-constexpr int kFew = 32;
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Calls f with the size of table that n tensors take.
+template <class F>
+cudaError_t with_table(int n, F f) {
+    return n <= 32 ? f(Int<32>{}) : n <= 128 ? f(Int<128>{}) : n <= 256 ? f(Int<256>{}) : n <= 512 ? f(Int<512>{})
+                                                                                             : f(Int<kCap>{});
+}
 
 long chunks_of(const moe_tensor_ref& r, long chunk) {
     if (r.numel == 0) return 0;
@@ -306,32 +318,46 @@ bool is_large(const moe_tensor_ref* refs, int n) {
 }
 
 template <int CAP, int U>
-cudaError_t launch_partials_of(const moe_tensor_ref* refs, int n, double* partial, int* n_partial, cudaStream_t stream) {
-    GradTable<CAP> tab;
-    *n_partial = 0;
-    for (int at = 0; fill(&tab, refs, n, &at, kChunk<U>);) {
-        const int grid = grid_of(tab.first[tab.n]);
-        cudaError_t e = launch_after(sumsq_kernel<CAP, U>, grid, kThreads, 0, stream, tab, partial + *n_partial);
-        *n_partial += grid;
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+cudaError_t launch_partial(const GradTable<CAP>& tab, double* partial, int* n_partial, cudaStream_t stream) {
+    const int grid = grid_of(tab.first[tab.n]);
+    double* to = partial + *n_partial;
+    *n_partial += grid;
+    return launch_after(sumsq_kernel<CAP, U>, grid, kThreads, 0, stream, tab, to);
 }
 
 template <int CAP>
 cudaError_t launch_partials(const moe_tensor_ref* refs, int n, bool large, double* partial, int* n_partial,
                             cudaStream_t stream) {
-    return large ? launch_partials_of<CAP, 8>(refs, n, partial, n_partial, stream)
-                 : launch_partials_of<CAP, 4>(refs, n, partial, n_partial, stream);
+    GradTable<CAP> tab;
+    *n_partial = 0;
+    cudaError_t e = cudaSuccess;
+    for (int at = 0; e == cudaSuccess && fill(&tab, refs, n, &at, large ? kChunk<8> : kChunk<kScaleU>);)
+        e = large ? launch_partial<CAP, 8>(tab, partial, n_partial, stream)
+                  : launch_partial<CAP, kScaleU>(tab, partial, n_partial, stream);
+    return e;
+}
+
+template <int CAP>
+cudaError_t launch_scale(const GradTable<CAP>& tab, bool large, const double* partial, int n_partial,
+                         const double* sumsq, float max_norm, float eps, float* norm, cudaStream_t stream) {
+    const int chunks = tab.first[tab.n];
+    return launch_after(scale_kernel<CAP>, chunks == 0 ? 1 : large ? chunks : grid_of(chunks), kThreads, 0, stream, tab,
+                        partial, n_partial, sumsq, max_norm, eps, norm);
 }
 
 template <int CAP>
 cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps, float* norm,
                         double* partial, cudaStream_t stream) {
     const bool large = is_large(refs, n);
-    int np = 0;
+    GradTable<CAP> tab;
+    int np = 0, at = 0;
+    cudaError_t e = cudaSuccess;
+    if (!sumsq && !large && n <= CAP) {  // one table for both launches
+        if (fill(&tab, refs, n, &at, kChunk<kScaleU>)) e = launch_partial<CAP, kScaleU>(tab, partial, &np, stream);
+        return e != cudaSuccess ? e : launch_scale(tab, false, partial, np, sumsq, max_norm, eps, norm, stream);
+    }
     if (!sumsq) {
-        cudaError_t e = launch_partials<CAP>(refs, n, large, partial, &np, stream);
+        e = launch_partials<CAP>(refs, n, large, partial, &np, stream);
         if (e == cudaSuccess && large) {  // one block adds the partial sums for all
             double* total = partial + np;
             e = launch_after(finish_kernel, 1, kThreads, 0, stream, partial, np, total, norm);
@@ -340,18 +366,12 @@ cudaError_t launch_clip(const moe_tensor_ref* refs, int n, const double* sumsq, 
         }
         if (e != cudaSuccess) return e;
     }
-    GradTable<CAP> tab;
     bool any = false;
-    for (int at = 0; fill(&tab, refs, n, &at, kChunk<kScaleU>); any = true) {
-        const int chunks = tab.first[tab.n];
-        cudaError_t e = launch_after(scale_kernel<CAP>, large ? chunks : grid_of(chunks), kThreads, 0, stream, tab,
-                                     partial, np, sumsq, max_norm, eps, any ? static_cast<float*>(nullptr) : norm);
-        if (e != cudaSuccess) return e;
-    }
-    // No values: the norm alone.
-    if (!any && norm)
-        return launch_after(scale_kernel<CAP>, 1, kThreads, 0, stream, tab, partial, np, sumsq, max_norm, eps, norm);
-    return cudaSuccess;
+    for (; e == cudaSuccess && fill(&tab, refs, n, &at, kChunk<kScaleU>); any = true)
+        e = launch_scale(tab, large, partial, np, sumsq, max_norm, eps, any ? nullptr : norm, stream);
+    if (e == cudaSuccess && !any && norm)  // no values: the norm alone (the table is empty)
+        e = launch_scale(tab, large, partial, np, sumsq, max_norm, eps, norm, stream);
+    return e;
 }
 
 }  // namespace
@@ -374,16 +394,16 @@ cudaError_t launch_grad_sumsq(const moe_tensor_ref* refs, int n, double* sumsq, 
     int np = 0;
     double* partial = static_cast<double*>(ws);
     const bool large = is_large(refs, n);
-    cudaError_t e = n <= kFew ? launch_partials<kFew>(refs, n, large, partial, &np, stream)
-                              : launch_partials<kCap>(refs, n, large, partial, &np, stream);
+    const cudaError_t e =
+        with_table(n, [&](auto cap) { return launch_partials<decltype(cap)::value>(refs, n, large, partial, &np, stream); });
     return e != cudaSuccess ? e : launch_after(finish_kernel, 1, kThreads, 0, stream, partial, np, sumsq, norm);
 }
 
 cudaError_t launch_grad_clip(const moe_tensor_ref* refs, int n, const double* sumsq, float max_norm, float eps,
                              float* norm, void* ws, cudaStream_t stream) {
-    double* partial = static_cast<double*>(ws);
-    return n <= kFew ? launch_clip<kFew>(refs, n, sumsq, max_norm, eps, norm, partial, stream)
-                     : launch_clip<kCap>(refs, n, sumsq, max_norm, eps, norm, partial, stream);
+    return with_table(n, [&](auto cap) {
+        return launch_clip<decltype(cap)::value>(refs, n, sumsq, max_norm, eps, norm, static_cast<double*>(ws), stream);
+    });
 }
 
 }  // namespace moe

@@ -76,6 +76,31 @@ def test_more_tensors_than_one_launch_takes():
         assert abs(float(moe.moe_grad_norm(ts)) - norm64(ts)) <= 6 * U32 * norm64(ts)
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 127, 128, 129, 256, 257, 511, 512, 513, 999, 1000, 1001, 2000, 2001])
+def test_every_size_of_table(n):
+    """Small tensors, some of them empty, with a long one among them."""
+    sizes = [(7 * i) % 53 for i in range(n)]
+    sizes[n // 2] = 70001
+    check_clip(tensors(sizes, [BF, F], n), 2.0)
+    ts = tensors(sizes, [HF], n + 1)
+    assert abs(float(moe.moe_grad_norm(ts)) - norm64(ts)) <= 6 * U32 * norm64(ts)
+    check_clip(ts, 1.0, tensors(sizes, [HF], n + 2))
+
+
+def test_large_lists_in_one_and_in_several_tables():
+    """Over 64 MB, where the sum and the scaling are cut differently."""
+    for sizes in ([40_000_001], [90_001] * 400, [20_011] * 1700 + [3, 0, 5_000_000]):
+        check_clip(tensors(sizes, [BF], len(sizes)), 1.0)
+        ts = tensors(sizes, [F], len(sizes))
+        total = moe.moe_grad_sumsq(ts)
+        assert abs(float(total) - norm64(ts) ** 2) <= 9 * U32 * norm64(ts) ** 2
+        before = [t.clone() for t in ts[:3]]
+        moe.moe_grad_clip(ts, 1.0, sumsq=total)
+        for t, b in zip(ts, before):
+            want = b.double() / (float(total) ** 0.5 + 1e-6)
+            assert ((t.double() - want).abs() <= 12 * U32 * want.abs()).all()
+
+
 def test_large_tensors():
     """More chunks than a grid has blocks, and an element past 2^31 (4.3 GB)."""
     check_clip(tensors([50_000_001, 30_000_000], [BF, F], 9), 1.0)
