@@ -560,7 +560,8 @@ MOE_API int moe_unpermute_bwd(const void* dout, const void* y_sorted, const int3
  *   sigmoid, renormalised: dl_j = scaling * q_j * (1 - s_j) * (G_j - sum_i G_i q_i)
  *   sigmoid, not:          dl_j = scaling * G_j * s_j * (1 - s_j)
  * and 0 for experts that were not chosen.  The selection bias and the groups
- * only choose: they have no gradient.
+ * only choose: they have no gradient.  Logits of -inf have a score of 0; a token
+ * whose scores are all 0 gets no gradient.
  *   logits    [T, E] f32 (read), topk_ids [T, K] i32 as the routing call wrote
  *             it.  An id outside [0, E) is a choice that does not exist: it
  *             takes no part, and sets MOE_STATUS_BAD_ID; an id given twice

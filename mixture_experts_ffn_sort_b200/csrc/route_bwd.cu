@@ -77,18 +77,20 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
         if (!RENORM && t < T)
             for (int e = j; e < E; e += G) lmax = fmaxf(lmax, __ldg(lg + e));
         lmax = group_max<G>(lmax);
+        if (lmax == -INFINITY) lmax = 0.f;  // no score above 0: no gradient (z = 0)
         s = here ? expf(l - lmax) : 0.f;
         float z = RENORM ? s : 0.f;
         if (!RENORM && t < T)
             for (int e = j; e < E; e += G) z += expf(__ldg(lg + e) - lmax);
-        rz = 1.f / group_sum<G>(z);
+        z = group_sum<G>(z);
+        rz = z == 0.f ? 0.f : 1.f / z;
         q = here ? s * rz : 0.f;
     } else {
         s = here ? sigmoid(l) : 0.f;
         q = s;
         if (RENORM) {
             const float sum = group_sum<G>(s);
-            q = sum > 0.f ? s / sum : 0.f;  // every score below fp32's range: no gradient
+            q = sum == 0.f ? 0.f : s / sum;  // every score below fp32's range: no gradient
         }
     }
     const float mean = SOFTMAX || RENORM ? group_sum<G>(gj * q) : 0.f;

@@ -138,6 +138,29 @@ def test_scores_far_out():
     assert ((got.double().cpu() - want).abs() <= bound + 1e-38).all()
 
 
+@pytest.mark.parametrize("score,renorm,scaling", VARIANTS)
+def test_masked_logits(score, renorm, scaling):
+    """Experts masked by -inf or the lowest value: chosen or not, they get no gradient; a token
+    whose chosen experts are all masked gets none at all.  NaN stays in its own row."""
+    lowest = torch.finfo(torch.float32).min
+    T, E, K = 8, 12, 4
+    lg, ids, dw, _ = data(T, E, K, 23)
+    masked = torch.ones((T, E), dtype=torch.bool).scatter_(1, ids.long(), False)
+    lg[:4] = torch.where(masked[:4], torch.tensor([float("-inf"), lowest, float("-inf"), lowest])[:, None], lg[:4])
+    lg[1, ids[1, 3]] = float("-inf")  # fewer experts left than choices
+    lg[2, ids[2].long()] = float("-inf")
+    lg[2] = float("-inf")
+    lg[5, ids[5, 0]] = float("nan")
+    cfg = dict(score=score, renormalize=renorm, scaling=scaling)
+    got = moe.moe_route_bwd(lg.cuda(), ids.cuda(), dw.cuda(), **cfg).cpu()
+    assert torch.isfinite(got[[0, 1, 2, 3, 4, 6, 7]]).all()
+    assert (got[2] == 0).all() and got[1, ids[1, 3]] == 0 and not torch.isfinite(got[5]).all()
+    assert (got[:2][masked[:2]] == 0).all()
+    rows = torch.tensor([0, 3, 4, 6, 7])
+    want, bound = exact(lg[rows].clamp(min=-1e4), ids[rows], dw[rows], score, renorm, scaling, None)
+    assert ((got[rows].double() - want).abs() <= bound + 1e-38).all()
+
+
 def test_stream_graph_and_refusals():
     lg, ids, dw, _ = (None if t is None else t.cuda() for t in data(70, 128, 6, 17))
     want = moe.moe_route_bwd(lg, ids, dw)
