@@ -76,6 +76,21 @@ def test_more_tensors_than_one_launch_takes():
         assert abs(float(moe.moe_grad_norm(ts)) - norm64(ts)) <= 6 * U32 * norm64(ts)
 
 
+@pytest.mark.parametrize("dtypes", [[BF], [HF], [F], [HF, F]])
+@pytest.mark.parametrize("sizes", [[262144 - 9], [262144], [8192] * 32, [8192] * 31 + [8193], [1] * 32, [1] * 33,
+                                   [0] * 40 + [5, 7], [131072, 1, 131000], [4088, 4096, 4104] * 10])
+def test_a_cluster_of_blocks_and_just_beyond(sizes, dtypes):
+    """Lists of about 32 chunks of 16 KB, which one launch clips."""
+    check_clip(tensors(sizes, dtypes, 31), 1.5)
+    check_clip(tensors(sizes, dtypes, 32), 1e9)
+    check_clip(tensors(sizes, dtypes, 33), 0.5, tensors(sizes, dtypes, 34))
+    check_clip(tensors(sizes, dtypes, 35), 0.5, tensors(sizes, dtypes, 36, offset=1))
+    # The norm of the one launch and that of the sum alone are the same number to fp64.
+    ts = tensors(sizes, dtypes, 37)
+    s = float(moe.moe_grad_sumsq(ts))
+    assert abs(float(moe.moe_grad_clip(ts, 1e9)) - math.sqrt(s)) <= U32 * math.sqrt(s) * 1.001
+
+
 @pytest.mark.parametrize("n", [31, 32, 33, 127, 128, 129, 256, 257, 511, 512, 513, 999, 1000, 1001, 2000, 2001])
 def test_every_size_of_table(n):
     """Small tensors, some of them empty, with a long one among them."""
@@ -163,9 +178,10 @@ def test_dense_in_another_order():
             moe.moe_grad_norm([bad])
 
 
-def test_stream_and_graphs_side_by_side():
+@pytest.mark.parametrize("sizes", [[20000, 333, 4], [900001, 77, 40000], [333] * 50, [50_000_000]])
+def test_stream_and_graphs_side_by_side(sizes):
     """Two captured graphs replayed at once on two streams, and a call on another stream."""
-    sets = [tensors([20000, 333, 4], [BF, F], s) for s in (21, 22)]
+    sets = [tensors(sizes, [BF, F], s) for s in (21, 22)]
     keep = [[t.clone() for t in ts] for ts in sets]
     want = [norm64(ts) for ts in sets]
     moe.moe_grad_clip(tensors([10], [F], 1), 1.0)
