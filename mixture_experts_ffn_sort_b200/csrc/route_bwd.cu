@@ -2,14 +2,13 @@
 // route weights of a token to its E logits, the choice held fixed.
 //
 // G lanes per token (8, 16 or 32, at least K), lane j holding choice j, so that
-// a warp has the loads of several tokens in flight.  The K
-// scores are recomputed from the K chosen logits (softmax relative to the
-// largest of them, which cancels; the full normaliser, when the weights are
-// not renormalised, needs the whole row), then dl_j = scaling * q_j *
-// (G_j - sum_i G_i q_i), times (1 - s_j) for sigmoid scores.  The rows of a
-// warp's tokens are written as zeros (or as the unchosen experts' softmax
-// term) and the K chosen gradients are stored over them, after the loads: zeros
-// that go first delay them (21.5 us against 19.1 us with a warp a token).
+// a warp has the loads of several tokens in flight.  The K scores are
+// recomputed from the K chosen logits (softmax relative to the largest of them,
+// which cancels), then dl_j = scaling * q_j * (G_j - sum_i G_i q_i), times
+// (1 - s_j) for sigmoid scores.  The rows of a warp's tokens are written as
+// zeros and the K chosen gradients are stored over them, after the loads: zeros
+// that go first delay them (21.5 us against 19.1 us with a warp a token).  The
+// full softmax needs the whole row and has a kernel of its own.
 //
 // 32768 tokens of 512 experts, top-10, sigmoid: 16.4 us, 6.2 TB/s of 67 MB
 // written and 35 MB read, since each of the ten scattered logits of a row
@@ -47,12 +46,30 @@ __device__ __forceinline__ void warp_zero(float* p, long n, int lane) {
     if (rest < n) p[rest] = 0.f;
 }
 
+// Choices of the same expert: the lowest lane of a token collects them.  (Each
+// carries `term`, the token's part of the row; it counts once.)  Returns
+// whether this lane has something to store.
+__device__ __forceinline__ bool collect(int token, int id, bool here, int lane, float term, float* d) {
+    const uint32_t same = __match_any_sync(kFull, here ? token * MOE_MAX_E + id : -1 - lane);
+    const bool first = here && (same & ((1u << lane) - 1u)) == 0;
+    if (__any_sync(kFull, here && !first)) {
+        float sum = *d;
+        for (int i = 0; i < 32; ++i) {
+            const float di = __shfl_sync(kFull, *d, i);
+            if (first && i != lane && ((same >> i) & 1u)) sum += di - term;
+        }
+        *d = sum;
+    }
+    return first;
+}
+
 template <bool SOFTMAX, bool RENORM, int G>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict__ logits,
                                                         const int32_t* __restrict__ ids,
                                                         const float* __restrict__ dw, int T, int E, int K,
                                                         float scaling, const uint8_t* __restrict__ zero_mask,
                                                         float* __restrict__ dlogits, int32_t* __restrict__ status) {
+    static_assert(!SOFTMAX || RENORM, "the full softmax has a kernel of its own");
     constexpr int TPW = 32 / G;  // tokens of a warp
     const int t0 = ((blockIdx.x * blockDim.x + threadIdx.x) >> 5) * TPW;
     grid_dependency_wait();
@@ -60,62 +77,83 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const float* __restrict_
     const int lane = threadIdx.x & 31, j = lane % G;
     const int t = t0 + lane / G;
     const bool on = j < K && t < T;
-    const float* lg = logits + static_cast<size_t>(t) * E;
-    float* out = dlogits + static_cast<size_t>(t) * E;
     const size_t o = static_cast<size_t>(t) * K + j;
 
     const int id = on ? __ldg(ids + o) : -1;
     const bool here = id >= 0 && id < E;
     if (on && !here) report_status(status, MOE_STATUS_BAD_ID);
-    const float g = on && !(zero_mask && zero_mask[o]) ? __ldg(dw + o) : 0.f;
-    const float gj = here ? g : 0.f;
-    const float l = here ? __ldg(lg + id) : -INFINITY;
+    const float g = here && !(zero_mask && zero_mask[o]) ? __ldg(dw + o) : 0.f;
+    const float l = here ? __ldg(logits + static_cast<size_t>(t) * E + id) : -INFINITY;
 
-    float s = 0.f, q = 0.f, lmax = 0.f, rz = 0.f;
+    float s;
     if (SOFTMAX) {
-        lmax = l;
-        if (!RENORM && t < T)
-            for (int e = j; e < E; e += G) lmax = fmaxf(lmax, __ldg(lg + e));
-        lmax = group_max<G>(lmax);
-        if (lmax == -INFINITY) lmax = 0.f;  // no score above 0: no gradient (z = 0)
+        float lmax = group_max<G>(l);
+        if (lmax == -INFINITY) lmax = 0.f;  // no score above 0
         s = here ? expf(l - lmax) : 0.f;
-        float z = RENORM ? s : 0.f;
-        if (!RENORM && t < T)
-            for (int e = j; e < E; e += G) z += expf(__ldg(lg + e) - lmax);
-        z = group_sum<G>(z);
-        rz = z == 0.f ? 0.f : 1.f / z;
-        q = here ? s * rz : 0.f;
     } else {
         s = here ? sigmoid(l) : 0.f;
-        q = s;
-        if (RENORM) {
-            const float sum = group_sum<G>(s);
-            q = sum == 0.f ? 0.f : s / sum;  // every score below fp32's range: no gradient
-        }
     }
-    const float mean = SOFTMAX || RENORM ? group_sum<G>(gj * q) : 0.f;
-    float d = scaling * q * (gj - mean);
+    float q = s, mean = 0.f;
+    if (RENORM) {
+        const float z = group_sum<G>(s);
+        q = z == 0.f ? 0.f : s / z;  // every score below fp32's range: no gradient
+        mean = group_sum<G>(g * q);
+    }
+    float d = scaling * q * (g - mean);
     if (!SOFTMAX) d *= here ? sigmoid(-l) : 0.f;  // 1 - s without the cancellation
-    if (SOFTMAX && !RENORM) {
-        if (t < T)
-            for (int e = j; e < E; e += G) out[e] = -scaling * (expf(__ldg(lg + e) - lmax) * rz) * mean;
-    } else {
-        warp_zero(dlogits + static_cast<size_t>(t0) * E, static_cast<long>(min(TPW, T - t0)) * E, lane);
-    }
-    // Choices of the same expert: the lowest lane collects them.
-    const uint32_t same = __match_any_sync(kFull, here ? (lane / G) * MOE_MAX_E + id : -1 - lane);
-    const bool first = here && (same & ((1u << lane) - 1u)) == 0;
-    if (__any_sync(kFull, here && !first)) {
-        // (Each choice of a full softmax carries the row's term; it counts once.)
-        const float term = SOFTMAX && !RENORM ? -scaling * q * mean : 0.f;
-        float sum = d;
-        for (int i = 0; i < 32; ++i) {
-            const float di = __shfl_sync(kFull, d, i);
-            if (first && i != lane && ((same >> i) & 1u)) sum += di - term;
-        }
-        d = sum;
-    }
+    warp_zero(dlogits + static_cast<size_t>(t0) * E, static_cast<long>(min(TPW, T - t0)) * E, lane);
+    const bool first = collect(lane / G, id, here, lane, 0.f, &d);
     __syncwarp();  // the rows' zeros before the chosen logits
+    if (first) dlogits[static_cast<size_t>(t) * E + id] = d;
+}
+
+// The softmax over all experts, not renormalised: every logit has a gradient.
+// One warp per token, which reads the row once and keeps its scores, EPL a
+// lane.  32768 tokens of 512 experts, top-10: 31.0 us, 4.3 TB/s of 134 MB (33.8
+// us with the row read for the maximum, the sum and the result); the exponentials
+// and the chain of four sums over the warp hold it back.
+template <int EPL>
+__global__ void __launch_bounds__(256) route_bwd_full_kernel(const float* __restrict__ logits,
+                                                             const int32_t* __restrict__ ids,
+                                                             const float* __restrict__ dw, int T, int E, int K,
+                                                             float scaling, const uint8_t* __restrict__ zero_mask,
+                                                             float* __restrict__ dlogits,
+                                                             int32_t* __restrict__ status) {
+    const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    if (t >= T) return;
+    const float* lg = logits + static_cast<size_t>(t) * E;
+    float* out = dlogits + static_cast<size_t>(t) * E;
+    const size_t o = static_cast<size_t>(t) * K + lane;
+
+    const int id = lane < K ? __ldg(ids + o) : -1;
+    float p[EPL], lmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) p[i] = lane + 32 * i < E ? __ldg(lg + lane + 32 * i) : -INFINITY;
+    const bool here = id >= 0 && id < E;
+    if (lane < K && !here) report_status(status, MOE_STATUS_BAD_ID);
+    const float g = here && !(zero_mask && zero_mask[o]) ? __ldg(dw + o) : 0.f;
+    const float l = here ? __ldg(lg + id) : -INFINITY;  // in L1 from the row
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) lmax = fmaxf(lmax, p[i]);
+    lmax = group_max<32>(lmax);
+    if (lmax == -INFINITY) lmax = 0.f;  // no score above 0: no gradient (z = 0)
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        p[i] = expf(p[i] - lmax);
+        z += p[i];
+    }
+    z = group_sum<32>(z);
+    const float rz = z == 0.f ? 0.f : 1.f / z;
+    const float q = here ? expf(l - lmax) * rz : 0.f;
+    const float mean = group_sum<32>(g * q), row = -scaling * mean;
+    float d = scaling * q * (g - mean);
+    const bool first = collect(0, id, here, lane, row * q, &d);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (lane + 32 * i < E) out[lane + 32 * i] = row * (p[i] * rz);
+    __syncwarp();  // the row before the chosen logits
     if (first) out[id] = d;
 }
 
@@ -130,8 +168,12 @@ cudaError_t launch_route_bwd(const float* logits, const int32_t* ids, const floa
                             zero_mask, dlogits, status);
     };
     if (cfg.score == MOE_SCORE_SOFTMAX) {
-        // The full softmax reads and writes whole rows: a warp for each.
-        if (!cfg.renormalize) return launch(route_bwd_kernel<true, false, 32>, 32);
+        if (!cfg.renormalize)
+            return E <= 64    ? launch(route_bwd_full_kernel<2>, 32)
+                   : E <= 128 ? launch(route_bwd_full_kernel<4>, 32)
+                   : E <= 256 ? launch(route_bwd_full_kernel<8>, 32)
+                   : E <= 512 ? launch(route_bwd_full_kernel<16>, 32)
+                              : launch(route_bwd_full_kernel<32>, 32);
         return K <= 8 ? launch(route_bwd_kernel<true, true, 8>, 8)
                       : K <= 16 ? launch(route_bwd_kernel<true, true, 16>, 16)
                                 : launch(route_bwd_kernel<true, true, 32>, 32);
