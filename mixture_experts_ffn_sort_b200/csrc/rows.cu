@@ -9,9 +9,9 @@
 // with MOE_STATUS_BAD_MAP.  All of it is bound by memory: a few operations for
 // every element read or written.
 //
-// Each kernel has two forms: rows whose bytes are a multiple of 16 are moved
-// by aligned 16-byte vectors, other rows by 4-byte words or shifted windows
-// (rows.cuh).
+// Each kernel has two forms: rows whose bytes are a multiple of 16 are moved by
+// aligned 16-byte vectors, other rows by 4-byte words, by elements or by shifted
+// blocks of 16 bytes (rows.cuh), whichever was fastest there.
 #include <type_traits>
 
 #include "launch.h"
@@ -141,10 +141,9 @@ __device__ __forceinline__ void slot_batch(const int32_t* __restrict__ inv, cons
 // out[t] = sum_j w[t, j] y[inv[t, j]] (+ y_shared[t]).  One thread per 16-byte
 // column of a token; slots in batches: all positions, then all rows, then the
 // sums in slot order, so that the loads of a batch (of at most B) are in flight
-// together.  SHIFT: rows that start anywhere, by shifted windows.  8192 bf16
-// rows of 4096, top-10: 135 us, which the ring below takes to 113 us; here are
-// the calls that are too small for it, bound by latency.
-template <class E, bool SHIFT, int B>
+// together.  8192 bf16 rows of 4096, top-10: 135 us, which the ring below takes
+// to 111 us; here are the calls that are too small for it, bound by latency.
+template <class E, int B>
 __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restrict__ y_sorted,
                                                              const int32_t* __restrict__ inv,
                                                              const float* __restrict__ w,
@@ -167,33 +166,27 @@ __global__ void __launch_bounds__(kThreads) unpermute_kernel(const char* __restr
             slot_batch(inv, w, t * K + j0, R, K - j0 < batch ? K - j0 : batch, p, wj, &bad);
             uint4 v[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                if (p[b] < 0) continue;
-                const long row = p[b] * row_bytes;
-                if (SHIFT) v[b] = load_window(y_sorted, row + 16 * c, R * row_bytes);
-                else v[b] = __ldg(reinterpret_cast<const uint4*>(y_sorted + row) + c);
-            }
+            for (int b = 0; b < B; ++b)
+                if (p[b] >= 0) v[b] = __ldg(reinterpret_cast<const uint4*>(y_sorted + p[b] * row_bytes) + c);
 #pragma unroll
             for (int b = 0; b < B; ++b)
                 if (p[b] >= 0) add_weighted<E>(acc, v[b], wj[b]);
         }
-        const long at = t * row_bytes + 16 * c;
         if (y_shared) {
             float f[N];
-            unpack<E>(SHIFT ? load_window(y_shared, at, T * row_bytes)
-                            : __ldg(reinterpret_cast<const uint4*>(y_shared + at)), f);
+            unpack<E>(__ldg(reinterpret_cast<const uint4*>(y_shared) + i), f);
 #pragma unroll
             for (int n = 0; n < N; ++n) acc[n] += f[n];
         }
-        if (SHIFT) store_part<E>(out + at, pack<E>(acc), 0, static_cast<int>((row_bytes - 16 * c) / sizeof(E)));
-        else *reinterpret_cast<uint4*>(out + at) = pack<E>(acc);
+        reinterpret_cast<uint4*>(out)[i] = pack<E>(acc);
     }
     if (bad) report_status(status, MOE_STATUS_BAD_MAP);
 }
 
-// The same for rows of a multiple of 4 bytes but not 16, by 4-byte words; a
-// thread has W of them, a warp's width apart.
-template <class E, int W>
+// The same for rows that are no multiple of 16 bytes, by 4-byte words where they
+// are a multiple of 4 and by elements (2 bytes) otherwise; a thread has W of
+// them, a warp's width apart.
+template <class E, class Word, int W>
 __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* __restrict__ y_sorted,
                                                                    const int32_t* __restrict__ inv,
                                                                    const float* __restrict__ w,
@@ -203,35 +196,38 @@ __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* _
                                                                    int32_t* __restrict__ status) {
     constexpr int B = kBatch;
     const long R = static_cast<long>(T) * K, total = static_cast<long>(T) * tiles.d * (W > 1 ? 32 : 1);
-    const int words = static_cast<int>(row_bytes >> 2);
+    constexpr int N = sizeof(Word) / sizeof(E);
+    const int words = static_cast<int>(row_bytes / sizeof(Word));
     bool bad = false;
     grid_dependency_wait();
     for (long i = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
          i += static_cast<long>(gridDim.x) * blockDim.x) {
         const long tile = W > 1 ? i >> 5 : i, t = tiles.div(tile);
         const int k0 = static_cast<int>(tile - t * tiles.d) * (W > 1 ? 32 * W : 1) + (W > 1 ? threadIdx.x & 31 : 0);
-        auto load = [&](const char* row, uint32_t (&v)[W]) {
+        auto load = [&](const char* row, Word (&v)[W]) {
 #pragma unroll
             for (int u = 0; u < W; ++u)
-                v[u] = k0 + 32 * u < words ? __ldg(reinterpret_cast<const uint32_t*>(row) + k0 + 32 * u) : 0;
+                v[u] = k0 + 32 * u < words ? __ldg(reinterpret_cast<const Word*>(row) + k0 + 32 * u) : Word(0);
         };
-        float acc[W][2];
+        float acc[W][N];
 #pragma unroll
-        for (int u = 0; u < W; ++u) acc[u][0] = acc[u][1] = 0.f;
-        auto add = [&](const uint32_t (&v)[W], float by) {
+        for (int u = 0; u < W; ++u)
+#pragma unroll
+            for (int n = 0; n < N; ++n) acc[u][n] = 0.f;
+        auto add = [&](const Word (&v)[W], float by) {
 #pragma unroll
             for (int u = 0; u < W; ++u) {
-                float f[2];
-                unpack_word<E>(v[u], f);
-                acc[u][0] = fmaf(by, f[0], acc[u][0]);
-                acc[u][1] = fmaf(by, f[1], acc[u][1]);
+                E e[N];
+                memcpy(e, &v[u], sizeof(Word));
+#pragma unroll
+                for (int n = 0; n < N; ++n) acc[u][n] = fmaf(by, elem_to_float(e[n]), acc[u][n]);
             }
         };
         for (int j0 = 0; j0 < K; j0 += batch) {
             int32_t p[B];
             float wj[B];
             slot_batch(inv, w, t * K + j0, R, K - j0 < batch ? K - j0 : batch, p, wj, &bad);
-            uint32_t v[B][W];
+            Word v[B][W];
 #pragma unroll
             for (int b = 0; b < B; ++b)
                 if (p[b] >= 0) load(y_sorted + p[b] * row_bytes, v[b]);
@@ -240,14 +236,19 @@ __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* _
                 if (p[b] >= 0) add(v[b], wj[b]);
         }
         if (y_shared) {
-            uint32_t v[W];
+            Word v[W];
             load(y_shared + t * row_bytes, v);
             add(v, 1.f);
         }
 #pragma unroll
-        for (int u = 0; u < W; ++u)
-            if (k0 + 32 * u < words)
-                reinterpret_cast<uint32_t*>(out + t * row_bytes)[k0 + 32 * u] = pack_word<E>(acc[u]);
+        for (int u = 0; u < W; ++u) {
+            E e[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) e[n] = elem_from_float<E>(acc[u][n]);
+            Word o;
+            memcpy(&o, e, sizeof(Word));
+            if (k0 + 32 * u < words) reinterpret_cast<Word*>(out + t * row_bytes)[k0 + 32 * u] = o;
+        }
     }
     if (bad) report_status(status, MOE_STATUS_BAD_MAP);
 }
@@ -694,22 +695,26 @@ int grid_for(long threads) {
 
 long row_bytes_of(const RowsArgs& a) { return static_cast<long>(a.H) * dtype_bytes(a.dtype); }
 
-// The words of a row at either start (RowWords), in tiles of one, or of four to
-// a lane of a warp when that leaves no warp short.
+// A row's words in tiles of one, or of W to each lane of a warp.
 struct WordTiles {
-    bool four;
     FastDiv div;  // tiles of a row
     int grid;
-    WordTiles(const RowsArgs& a, long row) : div(1) {
-        const long words = (row + (row % 4 ? 2 : 0) + 3) / 4;
-        four = words >= 128;
-        div = FastDiv(static_cast<unsigned>(four ? (words + 127) / 128 : words));
-        grid = grid_for(static_cast<long>(a.T) * div.d * (four ? 32 : 1));
+    WordTiles(const RowsArgs& a, long words, int W) : div(static_cast<unsigned>(W > 1 ? (words + 32 * W - 1) / (32 * W) : words)) {
+        grid = grid_for(static_cast<long>(a.T) * div.d * (W > 1 ? 32 : 1));
     }
 };
 
 template <int V>
 using Int = std::integral_constant<int, V>;
+
+// Calls f with the words that a thread takes of a row: as many as leave no more
+// than half of a warp's without work (20000 tokens of 97 elements, top-8: 16.6 us
+// with 4, 22.1 us with 2, 29.2 us with 1; 65536 of 61: 35.2 us with 2, 55.4 us
+// with 1).
+template <class F>
+auto with_words(long words, F f) {
+    return words > 96 ? f(Int<4>{}) : words > 32 ? f(Int<2>{}) : f(Int<1>{});
+}
 
 // Calls f(E, SHIFT) for the row type and alignment.
 template <class F>
@@ -733,13 +738,13 @@ cudaError_t launch_permute(const RowsArgs& a, const void* x, void* x_sorted, cud
         return launch_after(permute_kernel, grid_for(static_cast<long>(a.T) * vecs.d), kThreads, 0, stream, in, a.inv, a.n_rows, a.T, a.K,
                             row, vecs, out, a.status);
     }
-    const WordTiles tiles(a, row);
-    auto launch = [&](auto half, auto w) {
-        return launch_after(permute_words_kernel<decltype(half)::value, decltype(w)::value>, tiles.grid, kThreads, 0,
+    const long words = (row + (row % 4 ? 2 : 0) + 3) / 4;  // at either start
+    auto launch = [&](auto half, auto W) {
+        const WordTiles tiles(a, words, decltype(W)::value);
+        return launch_after(permute_words_kernel<decltype(half)::value, decltype(W)::value>, tiles.grid, kThreads, 0,
                             stream, in, a.inv, a.n_rows, a.T, a.K, row, tiles.div, out, a.status);
     };
-    if (row % 4) return tiles.four ? launch(std::true_type{}, Int<4>{}) : launch(std::true_type{}, Int<1>{});
-    return tiles.four ? launch(std::false_type{}, Int<4>{}) : launch(std::false_type{}, Int<1>{});
+    return with_words(words, [&](auto W) { return row % 4 ? launch(std::true_type{}, W) : launch(std::false_type{}, W); });
 }
 
 namespace {
@@ -794,32 +799,30 @@ cudaError_t launch_unpermute(const RowsArgs& a, const void* y_sorted, const floa
     auto even = [&](int most) { return (a.K + (a.K + most - 1) / most - 1) / ((a.K + most - 1) / most); };
     dispatch(a, [&](auto e, auto shift) {
         using E = decltype(e);
-        const FastDiv vecs(static_cast<unsigned>((row + 15) / 16));
-        const int grid = grid_for(static_cast<long>(a.T) * vecs.d);
-        auto vectors = [&](auto sh_, auto most) {
-            constexpr int B = decltype(most)::value;
-            err = launch_after(unpermute_kernel<E, decltype(sh_)::value, B>, grid, kThreads, 0, stream, y, a.inv, w, sh,
-                               a.T, a.K, even(B), row, vecs, to, a.status);
-        };
         if constexpr (!decltype(shift)::value) {
+            const FastDiv vecs(static_cast<unsigned>(row / 16));
+            const int grid = grid_for(static_cast<long>(a.T) * vecs.d);
+            auto vectors = [&](auto most) {
+                constexpr int B = decltype(most)::value;
+                err = launch_after(unpermute_kernel<E, B>, grid, kThreads, 0, stream, y, a.inv, w, sh, a.T, a.K, even(B),
+                                   row, vecs, to, a.status);
+            };
             // One wave of blocks: one batch of all slots is one wait less (64 tokens of width 2048,
             // top-8: 2.6 us against 2.8 us).  More: the registers of larger batches cost more warps
             // than the wait.
-            if (a.K > 4 && grid <= 148 * 3) vectors(shift, Int<8>{});
-            else vectors(shift, Int<kBatch>{});
+            if (a.K > 4 && grid <= 148 * 3) vectors(Int<8>{});
+            else vectors(Int<kBatch>{});
         } else {
-            // Rows that start within a word take more words than windows: 32768 tokens of width 301
-            // 118 us against 68 us; of width 300 58 us against 63 us (777 of 1030 4.2 us against 5.7 us).
-            if constexpr (sizeof(E) == 2) {
-                if (row % 4) return vectors(shift, Int<kBatch>{});
-            }
-            const WordTiles tiles(a, row);
-            auto words = [&](auto W) {
-                err = launch_after(unpermute_words_kernel<E, decltype(W)::value>, tiles.grid, kThreads, 0, stream, y,
-                                   a.inv, w, sh, a.T, a.K, even(kBatch), row, tiles.div, to, a.status);
+            auto words = [&](auto word, auto W) {
+                using Word = decltype(word);
+                const WordTiles tiles(a, row / static_cast<long>(sizeof(Word)), decltype(W)::value);
+                err = launch_after(unpermute_words_kernel<E, Word, decltype(W)::value>, tiles.grid, kThreads, 0, stream,
+                                   y, a.inv, w, sh, a.T, a.K, even(kBatch), row, tiles.div, to, a.status);
             };
-            if (tiles.four) words(Int<4>{});
-            else words(Int<1>{});
+            if constexpr (sizeof(E) == 2) {
+                if (row % 4) return with_words(a.H, [&](auto W) { words(uint16_t{}, W); });
+            }
+            with_words(row / 4, [&](auto W) { words(uint32_t{}, W); });
         }
     });
     return err;

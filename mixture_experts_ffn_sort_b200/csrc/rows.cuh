@@ -168,32 +168,6 @@ __device__ __forceinline__ void store_word(char* tensor, long at, long row_bytes
     }
 }
 
-// A word's elements (f32: one, the second is 0).
-template <class E>
-__device__ __forceinline__ void unpack_word(uint32_t v, float (&f)[2]) {
-    if constexpr (sizeof(E) == 4) {
-        f[0] = __uint_as_float(v);
-        f[1] = 0.f;
-    } else {
-        E e[2];
-        memcpy(e, &v, 4);
-        f[0] = elem_to_float(e[0]);
-        f[1] = elem_to_float(e[1]);
-    }
-}
-__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], __nv_bfloat16) { return pack_bf16x2(f[0], f[1]); }
-__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], __half) {
-    const __half2 h = __floats2half2_rn(f[0], f[1]);
-    uint32_t v;
-    memcpy(&v, &h, 4);
-    return v;
-}
-__device__ __forceinline__ uint32_t pack_word_as(const float (&f)[2], float) { return __float_as_uint(f[0]); }
-template <class E>
-__device__ __forceinline__ uint32_t pack_word(const float (&f)[2]) {
-    return pack_word_as(f, E{});
-}
-
 // The words at + 128 k (k = 0..3) of shared memory at any 2-byte place `at` of
 // `base` (16-byte aligned, 4 bytes of room after the last word).
 __device__ __forceinline__ uint4 load_shared_words(const char* base, int at) {
