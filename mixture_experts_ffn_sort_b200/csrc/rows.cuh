@@ -81,11 +81,11 @@ struct FastDiv {
 
 // ---------------------------------------------------------------- rows that do not start on 16 bytes
 //
-// When a row's bytes are no multiple of 16, rows start at every multiple of
-// their element.  The kernels then still move 16 bytes at a time: 16 bytes
-// from any place are two aligned loads and a shift, the second of them an L1
-// hit of the neighbouring thread's first.  Only the 16-byte blocks that
-// reach out of the whole tensor (its last one) are read element by element.
+// When a row's bytes are no multiple of 16, rows start at any multiple of their
+// element.  16 bytes from any place are two aligned blocks and a shift, the
+// second of them an L1 hit of the neighbouring thread's first; only a block that
+// reaches out of the whole tensor (its last one) is read element by element.
+// 4-byte words need a shift by half a word at most.
 
 __device__ __forceinline__ uint4 load_block(const char* base, long a, long total) {
     if (a >= 0 && a + 16 <= total) return __ldg(reinterpret_cast<const uint4*>(base + a));
