@@ -16,10 +16,10 @@
 // anything is scaled, so what does not fit L2 is read twice.
 #include <type_traits>
 
-#include "launch.h"
 #include "launch_after.cuh"
 #include "router_common.cuh"
 #include "rows.cuh"
+#include "train.h"
 
 namespace moe {
 

@@ -16,6 +16,7 @@
 #include "../../include/moe_ffn.h"
 #include "launch.h"
 #include "router.h"
+#include "train.h"
 
 namespace moe {
 bool ffn_decode_supported(int H, int I);

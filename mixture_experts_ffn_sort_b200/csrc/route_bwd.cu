@@ -13,9 +13,9 @@
 // 32768 tokens of 512 experts, top-10, sigmoid: 16.4 us, 6.2 TB/s of 67 MB
 // written and 35 MB read, since each of the ten scattered logits of a row
 // brings its whole piece of DRAM.
-#include "launch.h"
 #include "launch_after.cuh"
 #include "route_device.cuh"
+#include "train.h"
 
 namespace moe {
 

@@ -14,9 +14,9 @@
 // blocks of 16 bytes (rows.cuh), whichever was fastest there.
 #include <type_traits>
 
-#include "launch.h"
 #include "launch_after.cuh"
 #include "rows.cuh"
+#include "train.h"
 
 namespace moe {
 
