@@ -61,6 +61,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Called by a whole warp that has read a ring stage with ordinary loads
+// (ld.shared, ldmatrix), before the producer refills it by a bulk or TMA copy.
+// The copy writes through the async proxy, and an arrive orders the warp's
+// loads before it only behind a proxy fence: without one, loads still waiting
+// in the pipeline (an SM shared with a block that keeps its load path full)
+// read the refill.
+__device__ __forceinline__ void release_stage(uint64_t* empty, int lane) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty);
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(

@@ -567,8 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 else
                     stage_mma<NT>(tile, tile + kStageBytes / 2, lm_row, chunk_sel, b_lane + kb * 256, xstride,
                                   part[0]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.empty[st]);
+                release_stage(&s.empty[st], lane);
             }
             const float gs = __ldg(sg + kb), us = __ldg(su + kb);
 #pragma unroll
@@ -772,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     stage_mma_q<NT, true>(tile, tile, lm_row, chunk_sel, b_lane + kb * 128, hstride, part);
                 else
                     stage_mma<NT>(tile, tile, lm_row, chunk_sel, b_lane + kb * 256, hstride, part[0]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.empty[st]);
+                release_stage(&s.empty[st], lane);
             }
             const float ds = __ldg(sd + kb);
             if constexpr (Q) {
