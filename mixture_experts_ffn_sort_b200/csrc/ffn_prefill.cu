@@ -806,8 +806,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < NW; ++k) v[k] = 0;
                     }
-                    __syncwarp();
-                    if (g % kSPS == kSPS - 1 && lane == 0) mbar_arrive(&B->w_empty[sw]);
+                    if (g % kSPS == kSPS - 1) release_stage(&B->w_empty[sw], lane);
+                    else __syncwarp();
                     // The A slot is free once the MMAs that last read it have
                     // completed; the decode above overlapped that wait.
                     const int ss = static_cast<int>(g % C::kSS);  // step slot of this step
