@@ -489,8 +489,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) unpermute_ring_kernel(const R
                     for (int g = 0; g < kGroup; ++g)
                         if (mt[g].at >= 0) add_weighted<E>(acc, v[g], mt[g].w);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&head->empty[stage]);
+                release_stage(&head->empty[stage], lane);
                 if (++stage == a.stages) {
                     stage = 0;
                     parity ^= 1;
