@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) unpermute_words_kernel(const char* _
 //
 // 8192 bf16 rows of 4096, top-10: 111 us, 6.6 TB/s of 739 MB, with 73 % of the
 // issue slots in use (two teams 118 us, one 155 us: the sums of 16-bit rows
-// need the warps); of 4095: 131 us, bound by instructions.
+// need the warps); of 4095: 120 us, bound by instructions.
 
 constexpr int kConsumers = 8;  // warps of a team
 constexpr int kTeams = 3;
