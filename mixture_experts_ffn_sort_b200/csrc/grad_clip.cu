@@ -304,6 +304,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
                         float* __restrict__ norm_out) {
     __shared__ double warps[kClusterThreads / 32];
     __shared__ double blocks[kClusterBlocks];
+    cluster_arrive();  // waited for before the first store into another block
     const uint32_t rank = cluster_ctarank();
     const int c = static_cast<int>(rank) * (kClusterThreads / kThreads) + threadIdx.x / kThreads;
     const bool have = c < tab.first[tab.n];
@@ -330,6 +331,7 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
     for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = acc;
     __syncthreads();
+    cluster_wait();
     if (threadIdx.x < kClusterBlocks) {  // this block's sum, to every block of the cluster
         double sum = 0.;
         for (int w = 0; w < kClusterThreads / 32; ++w) sum += warps[w];
@@ -416,8 +418,9 @@ int grid_of(int chunks) { return chunks < kMaxBlocks ? chunks : kMaxBlocks; }
 constexpr long kLarge = 64L << 20;
 
 // Lists of as many chunks (16 KB or less) as a cluster has groups of threads are
-// clipped by one: 9 tensors of 8 KB in 4.0 us a call against 6.2 us, 4.1 us
-// against 4.5 us of it on the GPU.
+// clipped by one launch: 9 fp32 tensors of 8 KB take 3.9 us a call in a loop of
+// calls, which the host bounds, against 5.8 us with two launches, and 3.5 us
+// against 4.1 us of the GPU's time in a graph.
 constexpr int kClusterChunks = kClusterBlocks * kClusterThreads / kThreads;
 
 bool is_large(const moe_tensor_ref* refs, int n) {
