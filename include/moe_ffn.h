@@ -594,9 +594,11 @@ MOE_API int moe_route_bwd(const float* logits, const int32_t* topk_ids, const fl
  *   moe_grad_clip:  out = data * min(1, max_norm / (norm + eps)), rounded once,
  *     with norm = sqrt(*sumsq) for a sumsq from the caller (device memory), or
  *     of these tensors when sumsq is NULL.  *norm (f32, may be NULL) receives
- *     it.  As the formula says, a norm of infinity scales finite gradients to
- *     0, and one of NaN makes every gradient NaN; look at *norm to skip such
- *     a step.
+ *     it.  The factor comes from the f64 norm (which is finite for finite
+ *     gradients; *norm reads infinity where it is above fp32's range) and keeps
+ *     fp32's accuracy however small it is.  As the formula says, a sum of
+ *     squares of infinity scales finite gradients to 0, and one of NaN makes
+ *     every gradient NaN; look at *norm to skip such a step.
  *   refs, n    n >= 0 tensors; numel 0 is valid (data may then be NULL)
  *   workspace  moe_grad_workspace_bytes(n) bytes, any contents (moe_grad_clip
  *              with a sumsq needs none)

@@ -192,6 +192,29 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
     }
 }
 
+// What a value is multiplied by: a, then b.  b is 1 unless the factor is too
+// small for a normal fp32 number; then it is a power of two, and a in [1/2, 1)
+// has all of its bits.  Such a list is scaled element by element, by code of its
+// own (both factors for every vector: 728 us against 722 us for 769 bf16 tensors
+// of 2 MB).
+struct Factor {
+    float a, b;
+    __device__ __forceinline__ bool plain() const { return b == 1.f; }
+};
+
+// The factor for a sum of squares.
+__device__ __forceinline__ Factor clip_factor(double sumsq, float max_norm, float eps, double* norm) {
+    *norm = sqrt(sumsq);
+    const double ratio = static_cast<double>(max_norm) / (*norm + static_cast<double>(eps));
+    if (ratio >= 1. || *norm == 0.) return {1.f, 1.f};
+    const float f = static_cast<float>(ratio);
+    if (f < 0x1p-126f && ratio > 0.) {
+        const int e = max(ilogb(ratio) + 1, -149);
+        return {static_cast<float>(ldexp(ratio, -e)), ldexpf(1.f, e)};
+    }
+    return {f, 1.f};  // NaN stays NaN
+}
+
 template <class E>
 __device__ __forceinline__ uint4 scaled(const uint4& v, float f) {
     float g[kVec<E>];
@@ -201,13 +224,13 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, float f) {
     return pack<E>(g);
 }
 
-template <class E, int U>
-__device__ __forceinline__ void chunk_scale(const void* src, void* dst, long numel, long k, float f) {
+template <class E, int U, bool PLAIN>
+__device__ __forceinline__ void chunk_scale(const void* src, void* dst, long numel, long k, Factor f) {
     const Span<U> s = Span<U>::template of<E>(src, numel, k);
     const char* base = static_cast<const char*>(src) - s.skip;
     char* to = static_cast<char*>(dst) - s.skip;
     const bool together = (reinterpret_cast<uintptr_t>(to) & 15) == 0;  // src and dst share their offset
-    if (together) {
+    if (PLAIN && together) {
         uint4 v[U];
         const bool inside = s.inside();
 #pragma unroll
@@ -217,38 +240,31 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, long num
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (inside || (s.at(u) >= s.skip && s.at(u) + 16 <= s.end))
-                *reinterpret_cast<uint4*>(to + s.at(u)) = scaled<E>(v[u], f);
+                *reinterpret_cast<uint4*>(to + s.at(u)) = scaled<E>(v[u], f.a);
         if (!inside)
             part_elements<E, U>(s, [&](long b) {
                 *reinterpret_cast<E*>(to + b) =
-                    elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
+                    elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f.a);
             });
         return;
     }
-    // Another offset: element by element, neighbouring threads on neighbouring elements.
+    // Element by element, neighbouring threads on neighbouring elements.
     const long first = s.lo > s.skip ? s.lo : s.skip, past = s.lo + kChunk<U> < s.end ? s.lo + kChunk<U> : s.end;
 #pragma unroll 8
     for (long b = first + chunk_thread() * static_cast<long>(sizeof(E)); b < past; b += kThreads * sizeof(E))
         *reinterpret_cast<E*>(to + b) =
-            elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
+            elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f.a * (PLAIN ? 1.f : f.b));
 }
 
-// The factor for a sum of squares.
-__device__ __forceinline__ float clip_factor(double sumsq, float max_norm, float eps, double* norm) {
-    *norm = sqrt(sumsq);
-    const double ratio = static_cast<double>(max_norm) / (*norm + static_cast<double>(eps));
-    return ratio >= 1. || *norm == 0. ? 1.f : static_cast<float>(ratio);  // NaN stays NaN
-}
-
-template <int CAP>
-__device__ __forceinline__ void table_scale(const GradTable<CAP>& tab, int c, float f) {
+template <bool PLAIN, int CAP>
+__device__ __forceinline__ void table_scale(const GradTable<CAP>& tab, int c, Factor f) {
     const int i = tensor_of(tab, c);
     const long k = c - tab.first[i], n = tab.numel_type[i] >> 2;
-    if (f == 1.f && tab.src[i] == tab.dst[i]) return;  // in place, nothing to clip
+    if (PLAIN && f.a == 1.f && tab.src[i] == tab.dst[i]) return;  // in place, nothing to clip
     switch (tab.numel_type[i] & 3) {
-        case MOE_DTYPE_BF16: chunk_scale<__nv_bfloat16, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
-        case MOE_DTYPE_F16: chunk_scale<__half, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
-        default: chunk_scale<float, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
+        case MOE_DTYPE_BF16: chunk_scale<__nv_bfloat16, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
+        case MOE_DTYPE_F16: chunk_scale<__half, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
+        default: chunk_scale<float, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
     }
 }
 
@@ -261,11 +277,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
     grid_dependency_wait();  // the partial sums
     const double s = sumsq ? *sumsq : sum_partials(partial, n_partial, sh);
     double norm;
-    const float f = clip_factor(s, max_norm, eps, &norm);
+    const Factor f = clip_factor(s, max_norm, eps, &norm);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     const int chunks = tab.first[tab.n];
     // The last ones first: they may still be in L2 from the sum.
-    for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale(tab, chunks - 1 - b, f);
+    if (f.plain())
+        for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale<true>(tab, chunks - 1 - b, f);
+    else
+        for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale<false>(tab, chunks - 1 - b, f);
 }
 
 // Both steps for a small list, in one launch that reads it once: a cluster of
@@ -344,17 +363,19 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
 #pragma unroll
     for (int w = 0; w < kClusterBlocks; ++w) sum += blocks[w];
     double norm;
-    const float f = clip_factor(sum, max_norm, eps, &norm);
+    const Factor f = clip_factor(sum, max_norm, eps, &norm);
     if (norm_out && rank == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     char* dst = static_cast<char*>(tab.dst[i]);
-    if (!have || (f == 1.f && src == dst)) return;
-    if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
+    if (!have || (f.plain() && f.a == 1.f && src == dst)) return;
+    if (!f.plain()) {
+        table_scale<false>(tab, c, f);
+    } else if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
         char* to = dst - s.skip;
-        if (type == MOE_DTYPE_BF16) kept_scale<__nv_bfloat16>(s, base, to, v, f);
-        else if (type == MOE_DTYPE_F16) kept_scale<__half>(s, base, to, v, f);
-        else kept_scale<float>(s, base, to, v, f);
+        if (type == MOE_DTYPE_BF16) kept_scale<__nv_bfloat16>(s, base, to, v, f.a);
+        else if (type == MOE_DTYPE_F16) kept_scale<__half>(s, base, to, v, f.a);
+        else kept_scale<float>(s, base, to, v, f.a);
     } else {
-        table_scale(tab, c, f);
+        table_scale<true>(tab, c, f);
     }
 }
 
