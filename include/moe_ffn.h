@@ -591,7 +591,8 @@ MOE_API int moe_route_bwd(const float* logits, const int32_t* topk_ids, const fl
  *     overflow or vanish, and everything above that in fp64, in a fixed order.
  *     Ranks that hold different tensors add their sumsq values (an all-reduce)
  *     before clipping.
- *   moe_grad_clip:  out = data * min(1, max_norm / (norm + eps)), rounded once,
+ *   moe_grad_clip:  out = data * min(1, max_norm / (norm + eps)), rounded once
+ *     (a factor of 1 where max_norm, norm and eps are all 0),
  *     with norm = sqrt(*sumsq) for a sumsq from the caller (device memory), or
  *     of these tensors when sumsq is NULL.  *norm (f32, may be NULL) receives
  *     it.  The factor comes from the f64 norm (which is finite for finite

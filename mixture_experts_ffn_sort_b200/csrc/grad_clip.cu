@@ -205,8 +205,8 @@ struct Factor {
 // The factor for a sum of squares.
 __device__ __forceinline__ Factor clip_factor(double sumsq, float max_norm, float eps, double* norm) {
     *norm = sqrt(sumsq);
-    const double ratio = static_cast<double>(max_norm) / (*norm + static_cast<double>(eps));
-    if (ratio >= 1. || *norm == 0.) return {1.f, 1.f};
+    const double over = *norm + static_cast<double>(eps), ratio = static_cast<double>(max_norm) / over;
+    if (ratio >= 1. || over == 0.) return {1.f, 1.f};  // 0 / 0 clips nothing
     const float f = static_cast<float>(ratio);
     if (f < 0x1p-126f && ratio > 0.) {
         const int e = max(ilogb(ratio) + 1, -149);
