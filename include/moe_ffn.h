@@ -588,7 +588,9 @@ MOE_API int moe_route_bwd(const float* logits, const int32_t* topk_ids, const fl
  *   moe_grad_sumsq:  *sumsq = sum over all tensors of data[i]^2 (f64), and, where
  *     norm is not NULL, *norm = sqrt(*sumsq) (f32).  Squares of 4 to 8
  *     neighbouring values are added in fp32, or in fp64 where fp32 would
- *     overflow or vanish, and everything above that in fp64, in a fixed order.
+ *     overflow or vanish, and everything above that in fp64, in an order fixed
+ *     by the sizes and by where in memory each tensor starts (modulo 16 bytes):
+ *     the same values elsewhere may give other last bits.
  *     Ranks that hold different tensors add their sumsq values (an all-reduce)
  *     before clipping.
  *   moe_grad_clip:  out = data * min(1, max_norm / (norm + eps)), rounded once

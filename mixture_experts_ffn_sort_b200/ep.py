@@ -224,16 +224,28 @@ class ExpertParallelPrefill:
 
 # ---------------------------------------------------------------- training: the norm of sharded gradients
 
+def _counts_replicated(group=None) -> bool:
+    """Whether this rank adds the replicated gradients' sum to the group's: its first rank does."""
+    import torch.distributed as dist
+    if group is not None or (dist.is_available() and dist.is_initialized()):
+        return dist.get_rank(group) == 0
+    return True
+
+
 def clip_grad_norm(expert_grads, replicated_grads, max_norm: float, eps: float = 1e-6, group=None) -> torch.Tensor:
     """Clip one rank's gradients in place by the norm over all ranks: the
     expert gradients differ from rank to rank (their sums of squares are added
     over the group), the replicated ones (router, shared expert, already
     reduced) are the same on every rank and count once.  Returns the norm
     before clipping, f32 [] on the device; no host synchronisation.  Every
-    rank calls it, with an empty list where it has none."""
+    rank calls it, with an empty list where it has none.
+
+    The first rank alone adds the replicated sum: the last bits of a sum depend
+    on where in memory the tensors start, and ranks that each added their own
+    would clip by factors that differ, so that the replicas drift apart."""
     own, shared = list(expert_grads), list(replicated_grads)
     every = TensorList(own + shared)
-    total = reduce_partials(moe_grad_sumsq(own if own else TensorList([], device=every.device)), group)
-    if shared:
+    total = moe_grad_sumsq(own if own else TensorList([], device=every.device))
+    if shared and _counts_replicated(group):
         total = total + moe_grad_sumsq(shared)
-    return moe_grad_clip(every, max_norm, eps, sumsq=total)
+    return moe_grad_clip(every, max_norm, eps, sumsq=reduce_partials(total, group))
