@@ -503,7 +503,9 @@ class TensorList:
     memory, no two overlapping.  out: where moe_grad_clip writes the clipped
     tensors (same shapes, strides and types; None: in place).  Checked once,
     when the list is made; it holds the tensors, so a list made of
-    gradients that a later step replaces has to be made again."""
+    gradients that a later step replaces has to be made again.  A call refuses
+    a list one of whose tensors has got other memory or another type since
+    (by Tensor.data, set_ or Module.to)."""
 
     def __init__(self, tensors, out=None, device=None):
         self.tensors = list(tensors)

@@ -288,7 +288,25 @@ const char kRefs[] = "moe_tensor_refs";
 
 struct Refs {
     std::vector<moe_tensor_ref> refs;
+    std::vector<Tensor> tensors, outs;  // outs: empty in place
     int index;
+    // Refuses a list when one of its tensors has other memory, fewer values or
+    // another type than when it was checked (Tensor.data, set_, Module.to): the
+    // addresses in refs are then no longer its own.
+    void check_current() const {
+        for (size_t i = 0; i < tensors.size(); ++i)
+            if (!same(tensors[i], refs[i].data, refs[i]) || (!outs.empty() && !same(outs[i], refs[i].out, refs[i])))
+                refuse("tensor " + std::to_string(i) +
+                       " or its output has other memory or another type than when the list was made: make it again");
+    }
+
+  private:
+    static bool same(const Tensor& t, const void* data, const moe_tensor_ref& r) {
+        const ScalarType type = r.dtype == MOE_DTYPE_BF16  ? c10::kBFloat16
+                                : r.dtype == MOE_DTYPE_F16 ? c10::kHalf
+                                                           : c10::kFloat;
+        return t.const_data_ptr() == data && t.numel() == r.numel && t.scalar_type() == type;
+    }
 };
 
 void free_refs(PyObject* o) { delete static_cast<Refs*>(PyCapsule_GetPointer(o, kRefs)); }
@@ -303,25 +321,30 @@ PyObject* refs(PyObject*, PyObject* const* a, Py_ssize_t n) {
         auto r = std::make_unique<Refs>();
         r->index = static_cast<int>(PyLong_AsLong(a[2]));
         r->refs.resize(static_cast<size_t>(count) + 1);
+        r->tensors.reserve(static_cast<size_t>(count));
+        if (a[1] != a[0]) r->outs.reserve(static_cast<size_t>(count));
         for (Py_ssize_t i = 0; i < count; ++i) {
-            const std::string name = "tensor " + std::to_string(i);
-            const Tensor& t = tensor(PyList_GET_ITEM(a[0], i), name.c_str());
-            const Tensor& o = tensor(PyList_GET_ITEM(a[1], i), name.c_str());
+            const auto name = [i] { return "tensor " + std::to_string(i); };
+            PyObject *pt = PyList_GET_ITEM(a[0], i), *po = PyList_GET_ITEM(a[1], i);
+            if (!THPVariable_Check(pt) || !THPVariable_Check(po)) refuse(name() + " and its output must be tensors");
+            const Tensor &t = THPVariable_Unpack(pt), &o = THPVariable_Unpack(po);
             int type = -1;
             switch (t.scalar_type()) {
                 case c10::kBFloat16: type = MOE_DTYPE_BF16; break;
                 case c10::kHalf: type = MOE_DTYPE_F16; break;
                 case c10::kFloat: type = MOE_DTYPE_F32; break;
-                default: refuse(name + " must be bfloat16, float16 or float32, not " + c10::toString(t.scalar_type()));
+                default: refuse(name() + " must be bfloat16, float16 or float32, not " + c10::toString(t.scalar_type()));
             }
             if (!t.is_cuda() || t.get_device() != r->index || !o.is_cuda() || o.get_device() != r->index)
-                refuse(name + ": the tensors and outputs must be CUDA tensors on one device");
+                refuse(name() + ": the tensors and outputs must be CUDA tensors on one device");
             if (!t.is_non_overlapping_and_dense())
-                refuse(name + " must be dense in memory (strides " + text(t.strides()) + ")");
+                refuse(name() + " must be dense in memory (strides " + text(t.strides()) + ")");
             if (!t.is_same(o) && (o.scalar_type() != t.scalar_type() || o.sizes() != t.sizes() ||
                                   (t.numel() && o.strides() != t.strides())))
                 refuse("output " + std::to_string(i) + " must have the shape, strides and type of its tensor");
             r->refs[static_cast<size_t>(i)] = {t.data_ptr(), o.data_ptr(), t.numel(), type, 0};
+            r->tensors.push_back(t);
+            if (a[1] != a[0]) r->outs.push_back(o);
         }
         check(moe_grad_refs_check(r->refs.data(), to_int(count, "the number of tensors")));
         return PyCapsule_New(r.release(), kRefs, free_refs);
@@ -338,6 +361,7 @@ const Refs& unwrap(PyObject* o) {
 PyObject* grad_sumsq(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 2, [&] {
         const Refs& r = unwrap(a[0]);
+        r.check_current();
         const Call c(r.index);
         const int count = static_cast<int>(r.refs.size()) - 1;
         float* norm = a[1] == Py_None ? nullptr
@@ -357,6 +381,7 @@ PyObject* grad_sumsq(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&] {
         const Refs& r = unwrap(a[0]);
+        r.check_current();
         const Call c(r.index);
         const int count = static_cast<int>(r.refs.size()) - 1;
         const float max_norm = static_cast<float>(PyFloat_AsDouble(a[1]));
