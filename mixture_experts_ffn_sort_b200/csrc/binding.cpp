@@ -54,6 +54,15 @@ const Tensor& tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
+// Marks a caller's tensor as changed in place, so that autograd refuses a
+// backward pass that saved what it held.  (Inference tensors have no such mark.)
+void changed(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void changed_if_given(PyObject* o, const Tensor& t) {
+    if (o != Py_None) changed(t);
+}
+
 // The device of the call's first tensor; its current stream is the call's.
 struct Call {
     int index;
@@ -180,6 +189,7 @@ PyObject* permute(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor out = c.out(a[3], "x_sorted", x.scalar_type(), {R, H});
         const int t = to_int(T, "T"), h = to_int(H, "H");
         launch([&] { return moe_permute(px, pi, rows, t, K, h, type, out.data_ptr(), st, c.stream()); });
+        changed_if_given(a[3], out);
         return THPVariable_Wrap(out);
     });
 }
@@ -204,6 +214,7 @@ PyObject* unpermute(PyObject*, PyObject* const* a, Py_ssize_t n) {
         int32_t* st = c.status(a[6]);
         const Tensor out = c.out(a[5], "out", row, {T, H});
         launch([&] { return moe_unpermute(py, pi, w, sh, t, K, h, type, out.data_ptr(), st, c.stream()); });
+        changed_if_given(a[5], out);
         return THPVariable_Wrap(out);
     });
 }
@@ -239,6 +250,8 @@ PyObject* unpermute_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
             void* pdy = need_dy ? dy.data_ptr() : nullptr;
             float* pdw = need_dw ? static_cast<float*>(dw.data_ptr()) : nullptr;
             launch([&] { return moe_unpermute_bwd(pd, py, pi, pw, rows, t, k, h, type, pdy, pdw, st, c.stream()); });
+            if (need_dy) changed_if_given(a[7], dy);
+            if (need_dw) changed_if_given(a[8], dw);
         }
         PyObject* pair = PyTuple_New(2);
         if (!pair) return nullptr;
@@ -278,6 +291,7 @@ PyObject* route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         launch([&] {
             return moe_route_bwd(pl, pi, pw, t, e, k, &cfg, mask, static_cast<float*>(out.data_ptr()), st, c.stream());
         });
+        changed_if_given(a[9], out);
         return THPVariable_Wrap(out);
     });
 }
@@ -373,6 +387,7 @@ PyObject* grad_sumsq(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return moe_grad_sumsq(r.refs.data(), count, static_cast<double*>(sumsq.data_ptr()), norm, ws.data_ptr(),
                                   need, c.stream());
         });
+        if (norm) changed(tensor(a[1], "norm"));
         return THPVariable_Wrap(sumsq);
     });
 }
@@ -398,6 +413,7 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return moe_grad_clip(r.refs.data(), count, given, max_norm, eps, static_cast<float*>(norm.data_ptr()),
                                  work, need, c.stream());
         });
+        for (const Tensor& t : r.outs.empty() ? r.tensors : r.outs) changed(t);
         return THPVariable_Wrap(norm);
     });
 }
