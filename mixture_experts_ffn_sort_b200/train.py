@@ -21,7 +21,7 @@ leaves is alive.
 from __future__ import annotations
 
 from dataclasses import dataclass
-from typing import Callable, Iterable, Optional
+from typing import Callable, Iterable, Optional, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -196,9 +196,12 @@ class RoutedLayer(torch.nn.Module):
         return unpermute(y, w, plan, None if self.shared is None else self.shared(x))
 
 
-def clip_grad_norm(parameters: Iterable[torch.nn.Parameter], max_norm: float, eps: float = 1e-6) -> torch.Tensor:
-    """Clip the parameters' gradients in place by their global 2-norm; returns
-    the norm before that, f32 [] on the device (no host synchronisation).
-    Parameters without a gradient are passed over; expert gradients that other
-    ranks hold are ep.clip_grad_norm's."""
+def clip_grad_norm(parameters: Union[torch.Tensor, Iterable[torch.Tensor]], max_norm: float,
+                   eps: float = 1e-6) -> torch.Tensor:
+    """Clip the parameters' gradients (or one parameter's) in place by their
+    global 2-norm; returns the norm before that, f32 [] on the device (no host
+    synchronisation).  Parameters without a gradient are passed over; expert
+    gradients that other ranks hold are ep.clip_grad_norm's."""
+    if isinstance(parameters, torch.Tensor):  # not its rows, which have no gradients of their own
+        parameters = [parameters]
     return moe_grad_clip([p.grad for p in parameters if p.grad is not None], max_norm, eps)
