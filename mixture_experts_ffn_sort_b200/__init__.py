@@ -456,6 +456,8 @@ def moe_unpermute(y_sorted: torch.Tensor, inv_route: torch.Tensor, topk_w: torch
     their weight already.)"""
     if topk_w is None:
         raise ValueError("topk_w must be a tensor (moe_permute_bwd adds rows without weights)")
+    if topk_w.dim() != 2:  # its first dimension says how many tokens there are
+        raise ValueError("topk_w must be [T, K], not %s" % (tuple(topk_w.shape),))
     if stream is not None:
         with _on(stream, y_sorted.device):
             return moe_unpermute(y_sorted, inv_route, topk_w, y_shared, out, status)
