@@ -83,6 +83,12 @@ def route(logits: torch.Tensor, K: int, score: int = MOE_SCORE_SOFTMAX, sel_bias
     return _Route.apply(_base(logits), K, _mask(zero_mask), cfg)
 
 
+def _product(a: torch.Tensor, b: torch.Tensor) -> torch.Tensor:
+    """a @ b in fp32, in an autocast region too (there the product would be rounded to 16 bits)."""
+    with torch.autocast("cuda", enabled=False):
+        return a.float() @ b.float()
+
+
 def _mask(zero_mask):
     if zero_mask is None:
         return None
@@ -106,8 +112,8 @@ class _Router(torch.autograd.Function):
         x, w_router, logits, ids, zero_mask = ctx.saved_tensors
         dlogits = moe_route_bwd(logits, ids, _base(dw), zero_mask=zero_mask, **ctx.cfg)
         # The gate GEMM's own gradients: two plain products, in fp32 like its logits.
-        dx = (dlogits @ w_router.float()).to(x.dtype) if ctx.needs_input_grad[0] else None
-        dwr = (dlogits.t() @ x.float()).to(w_router.dtype) if ctx.needs_input_grad[1] else None
+        dx = _product(dlogits, w_router).to(x.dtype) if ctx.needs_input_grad[0] else None
+        dwr = _product(dlogits.t(), x).to(w_router.dtype) if ctx.needs_input_grad[1] else None
         return dx, dwr, None, None, None
 
 
@@ -190,7 +196,7 @@ class RoutedLayer(torch.nn.Module):
         if self.fused_router() and x.dtype == torch.bfloat16:
             ids, w = router(x, self.w_router, self.top_k, zero_mask=zero_mask, **self.route_cfg)
         else:
-            ids, w = route(x.float() @ self.w_router.float().t(), self.top_k, zero_mask=zero_mask, **self.route_cfg)
+            ids, w = route(_product(x, self.w_router.t()), self.top_k, zero_mask=zero_mask, **self.route_cfg)
         self.plan = plan = sort_plan(ids, self.n_experts)
         y = self.experts(permute(x, plan), plan.expert_offsets)
         return unpermute(y, w, plan, None if self.shared is None else self.shared(x))
