@@ -47,9 +47,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or _stale(LIB, deps + [__file__]):
         _build_library(deps, force, verbose)
     binding = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "moe_ffn.h"), __file__]
-    if force or _stale(BINDING, binding):
+    if force or _stale(BINDING, binding) or _recorded() != _versions():
         _build_binding(binding[0], verbose)
     return LIB
+
+
+# What the binding was built for: it is compiled against torch's C++ headers and
+# Python's, and must not be loaded beside others.
+BUILT_FOR = os.path.join(OBJ_DIR, "binding.txt")
+
+
+def _versions() -> str:
+    from importlib.metadata import version
+    return "torch %s, Python %s" % (version("torch"), sys.version.split()[0])
+
+
+def _recorded() -> str:
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read()
+    except OSError:
+        return ""
 
 
 def _build_binding(src: str, verbose: bool):
@@ -72,6 +90,9 @@ def _build_binding(src: str, verbose: bool):
     if verbose and r.stderr:
         sys.stderr.write(r.stderr)
     os.replace(tmp, BINDING)
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(BUILT_FOR, "w") as f:
+        f.write(_versions())
 
 
 def _build_library(deps, force: bool, verbose: bool):
