@@ -292,9 +292,21 @@ constexpr int kShiftPad = 64;
 static_assert(kConsumers * kGroup <= 32, "a lane for every row of a stage");
 static_assert(kRingBytes / (kConsumers * kGroup * (512 + kShiftPad)) >= kProducers, "the ring has too few stages");
 // Taken for rows of at least kRingMinRow bytes and sorted rows of so many bytes
-// in all, where it overtakes the plain kernel, which starts faster: 42 MB 14.1
-// us against 11.9 us, 84 MB 20.3 us against 21.5 us; rows of 4095 elements 42 MB
-// 16.5 us against 20.1 us; rows of 512 bytes 33.2 us against 31.6 us (134 MB).
+// in all, where it overtakes the plain kernel, which starts faster.  Plain kernel
+// against ring, us, the same call again and again (up to about 100 MB from L2):
+//   bf16 x 4096, top-1:   32 MB 17.6 / 17.0   64 MB 43.8 / 32.3   160 MB 97 / 75
+//                top-10:  48 MB  9.3 /  9.6   64 MB 11.6 / 11.9    96 MB 23.8 / 19.0
+//                top-16:  48 MB  8.8 /  9.2   64 MB 10.2 / 12.4    96 MB 19.9 / 17.0
+//   f32 x 4096,  top-1:   32 MB 15.5 / 15.6   64 MB 40.2 / 29.5   160 MB 90 / 68
+//                top-10:  48 MB  7.3 /  7.9   64 MB  9.0 /  9.7    96 MB 22.1 / 17.4
+//   bf16 x 4095, top-1:   16 MB 17.4 / 12.9   32 MB 30.2 / 22.8   160 MB 166 / 102
+//                top-10:  16 MB  6.8 /  5.8   32 MB 11.7 /  8.9   160 MB 63 / 35
+//                top-16:  32 MB 10.3 / 11.1   48 MB 15.0 / 11.4   160 MB 54 / 31
+// With one or two rows a token it pays earlier than the rule says.  Rows of 2 KB
+// that do not start on 16 bytes are better off without it for most K, which the
+// rule does not look at (bf16 x 1030: top-4 64 MB 20.2 / 22.4, 96 MB 33.8 / 33.4;
+// top-10 32 MB 8.3 / 13.8, 160 MB 45.7 / 49.4; f32 x 1031, top-10 96 MB 24.7 /
+// 27.3), and rows of 512 bytes always (134 MB 31.6 / 33.2).
 constexpr long kRingMinRow = 1024;
 constexpr long kRingMinBytes = 64L << 20, kRingMinBytesShift = 24L << 20;
 
