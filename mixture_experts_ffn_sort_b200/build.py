@@ -58,8 +58,8 @@ BUILT_FOR = os.path.join(OBJ_DIR, "binding.txt")
 
 
 def _versions() -> str:
-    from importlib.metadata import version
-    return "torch %s, Python %s" % (version("torch"), sys.version.split()[0])
+    import torch  # its own word: a source build may have no package metadata
+    return "torch %s, Python %s" % (torch.__version__, sys.version.split()[0])
 
 
 def _recorded() -> str:

@@ -28,3 +28,14 @@ def test_no_record(built, monkeypatch, tmp_path):
     monkeypatch.setattr(build, "BUILT_FOR", str(tmp_path / "none.txt"), raising=False)
     build.build()
     assert built == ["binding"]
+
+
+def test_a_torch_without_package_metadata(built, monkeypatch):
+    import importlib.metadata
+
+    def none(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(importlib.metadata, "version", none)
+    build.build()
+    assert built == []
