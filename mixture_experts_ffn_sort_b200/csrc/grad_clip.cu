@@ -192,28 +192,15 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const double* __restri
     }
 }
 
-// What a value is multiplied by: a, then b.  b is 1 unless the factor is too
-// small for a normal fp32 number; then it is a power of two, and a in [1/2, 1)
-// has all of its bits.  Such a list is scaled element by element, by code of its
-// own (both factors for every vector: 728 us against 722 us for 769 bf16 tensors
-// of 2 MB).
-struct Factor {
-    float a, b;
-    __device__ __forceinline__ bool plain() const { return b == 1.f; }
-};
-
 // The factor for a sum of squares.
-__device__ __forceinline__ Factor clip_factor(double sumsq, float max_norm, float eps, double* norm) {
+__device__ __forceinline__ double clip_factor(double sumsq, float max_norm, float eps, double* norm) {
     *norm = sqrt(sumsq);
     const double over = *norm + static_cast<double>(eps), ratio = static_cast<double>(max_norm) / over;
-    if (ratio >= 1. || over == 0.) return {1.f, 1.f};  // 0 / 0 clips nothing
-    const float f = static_cast<float>(ratio);
-    if (f < 0x1p-126f && ratio > 0.) {
-        const int e = max(ilogb(ratio) + 1, -149);
-        return {static_cast<float>(ldexp(ratio, -e)), ldexpf(1.f, e)};
-    }
-    return {f, 1.f};  // NaN stays NaN
+    return ratio >= 1. || over == 0. ? 1. : ratio;  // 0 / 0 clips nothing, NaN stays NaN
 }
+
+// Whether the factor, rounded to fp32 as f, is too small for one of its normal numbers.
+__device__ __forceinline__ bool subnormal(float f, double ratio) { return f < 0x1p-126f && ratio > 0.; }
 
 template <class E>
 __device__ __forceinline__ uint4 scaled(const uint4& v, float f) {
@@ -224,13 +211,13 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, float f) {
     return pack<E>(g);
 }
 
-template <class E, int U, bool PLAIN>
-__device__ __forceinline__ void chunk_scale(const void* src, void* dst, long numel, long k, Factor f) {
+template <class E, int U>
+__device__ __forceinline__ void chunk_scale(const void* src, void* dst, long numel, long k, float f) {
     const Span<U> s = Span<U>::template of<E>(src, numel, k);
     const char* base = static_cast<const char*>(src) - s.skip;
     char* to = static_cast<char*>(dst) - s.skip;
     const bool together = (reinterpret_cast<uintptr_t>(to) & 15) == 0;  // src and dst share their offset
-    if (PLAIN && together) {
+    if (together) {
         uint4 v[U];
         const bool inside = s.inside();
 #pragma unroll
@@ -240,31 +227,61 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, long num
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (inside || (s.at(u) >= s.skip && s.at(u) + 16 <= s.end))
-                *reinterpret_cast<uint4*>(to + s.at(u)) = scaled<E>(v[u], f.a);
+                *reinterpret_cast<uint4*>(to + s.at(u)) = scaled<E>(v[u], f);
         if (!inside)
             part_elements<E, U>(s, [&](long b) {
                 *reinterpret_cast<E*>(to + b) =
-                    elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f.a);
+                    elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
             });
         return;
     }
-    // Element by element, neighbouring threads on neighbouring elements.
+    // Another offset: element by element, neighbouring threads on neighbouring elements.
     const long first = s.lo > s.skip ? s.lo : s.skip, past = s.lo + kChunk<U> < s.end ? s.lo + kChunk<U> : s.end;
 #pragma unroll 8
     for (long b = first + chunk_thread() * static_cast<long>(sizeof(E)); b < past; b += kThreads * sizeof(E))
         *reinterpret_cast<E*>(to + b) =
-            elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f.a * (PLAIN ? 1.f : f.b));
+            elem_from_float<E>(elem_to_float(*reinterpret_cast<const E*>(base + b)) * f);
 }
 
-template <bool PLAIN, int CAP>
-__device__ __forceinline__ void table_scale(const GradTable<CAP>& tab, int c, Factor f) {
+template <int CAP>
+__device__ __forceinline__ void table_scale(const GradTable<CAP>& tab, int c, float f) {
     const int i = tensor_of(tab, c);
     const long k = c - tab.first[i], n = tab.numel_type[i] >> 2;
-    if (PLAIN && f.a == 1.f && tab.src[i] == tab.dst[i]) return;  // in place, nothing to clip
+    if (f == 1.f && tab.src[i] == tab.dst[i]) return;  // in place, nothing to clip
     switch (tab.numel_type[i] & 3) {
-        case MOE_DTYPE_BF16: chunk_scale<__nv_bfloat16, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
-        case MOE_DTYPE_F16: chunk_scale<__half, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
-        default: chunk_scale<float, kScaleU, PLAIN>(tab.src[i], tab.dst[i], n, k, f); break;
+        case MOE_DTYPE_BF16: chunk_scale<__nv_bfloat16, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
+        case MOE_DTYPE_F16: chunk_scale<__half, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
+        default: chunk_scale<float, kScaleU>(tab.src[i], tab.dst[i], n, k, f); break;
+    }
+}
+
+template <class E>
+__device__ __forceinline__ void chunk_scale_small(const void* src, void* dst, long numel, long k, float a, float b) {
+    const Span<kScaleU> s = Span<kScaleU>::template of<E>(src, numel, k);
+    const long per = kChunk<kScaleU> / static_cast<long>(sizeof(E)), lead = s.skip / static_cast<long>(sizeof(E));
+    const long first = k * per > lead ? k * per - lead : 0;
+    const long past = (k + 1) * per - lead < numel ? (k + 1) * per - lead : numel;
+    for (long i = first + chunk_thread(); i < past; i += kThreads)
+        static_cast<E*>(dst)[i] = elem_from_float<E>(elem_to_float(static_cast<const E*>(src)[i]) * a * b);
+}
+
+// Chunks c, c - step, ... of the table (this thread's share) by a factor below
+// fp32's normal numbers: a, which has all of its bits, then b, a power of two.
+// Not inlined, and element by element, because it is hardly ever taken: as a
+// second factor for every vector it took 769 bf16 tensors of 2 MB from 719 to 728
+// us, inlined beside the other loop to 722 us.
+template <int CAP>
+__device__ __noinline__ void table_scale_small(const GradTable<CAP>& tab, int c, int step, double ratio) {
+    const int e = max(ilogb(ratio) + 1, -149);
+    const float a = static_cast<float>(ldexp(ratio, -e)), b = ldexpf(1.f, e);
+    for (; c >= 0; c -= step) {
+        const int i = tensor_of(tab, c);
+        const long k = c - tab.first[i], n = tab.numel_type[i] >> 2;
+        switch (tab.numel_type[i] & 3) {
+            case MOE_DTYPE_BF16: chunk_scale_small<__nv_bfloat16>(tab.src[i], tab.dst[i], n, k, a, b); break;
+            case MOE_DTYPE_F16: chunk_scale_small<__half>(tab.src[i], tab.dst[i], n, k, a, b); break;
+            default: chunk_scale_small<float>(tab.src[i], tab.dst[i], n, k, a, b); break;
+        }
     }
 }
 
@@ -277,14 +294,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) scale_kernel(const __grid_co
     grid_dependency_wait();  // the partial sums
     const double s = sumsq ? *sumsq : sum_partials(partial, n_partial, sh);
     double norm;
-    const Factor f = clip_factor(s, max_norm, eps, &norm);
+    const double ratio = clip_factor(s, max_norm, eps, &norm);
+    const float f = static_cast<float>(ratio);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     const int chunks = tab.first[tab.n];
     // The last ones first: they may still be in L2 from the sum.
-    if (f.plain())
-        for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale<true>(tab, chunks - 1 - b, f);
-    else
-        for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale<false>(tab, chunks - 1 - b, f);
+    if (subnormal(f, ratio)) return table_scale_small(tab, chunks - 1 - static_cast<int>(blockIdx.x), gridDim.x, ratio);
+    for (int b = blockIdx.x; b < chunks; b += gridDim.x) table_scale(tab, chunks - 1 - b, f);
 }
 
 // Both steps for a small list, in one launch that reads it once: a cluster of
@@ -363,19 +379,20 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
 #pragma unroll
     for (int w = 0; w < kClusterBlocks; ++w) sum += blocks[w];
     double norm;
-    const Factor f = clip_factor(sum, max_norm, eps, &norm);
+    const double ratio = clip_factor(sum, max_norm, eps, &norm);
+    const float f = static_cast<float>(ratio);
     if (norm_out && rank == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
     char* dst = static_cast<char*>(tab.dst[i]);
-    if (!have || (f.plain() && f.a == 1.f && src == dst)) return;
-    if (!f.plain()) {
-        table_scale<false>(tab, c, f);
+    if (!have || (f == 1.f && src == dst)) return;
+    if (subnormal(f, ratio)) {
+        table_scale_small(tab, c, c + 1, ratio);
     } else if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) == 0) {
         char* to = dst - s.skip;
-        if (type == MOE_DTYPE_BF16) kept_scale<__nv_bfloat16>(s, base, to, v, f.a);
-        else if (type == MOE_DTYPE_F16) kept_scale<__half>(s, base, to, v, f.a);
-        else kept_scale<float>(s, base, to, v, f.a);
+        if (type == MOE_DTYPE_BF16) kept_scale<__nv_bfloat16>(s, base, to, v, f);
+        else if (type == MOE_DTYPE_F16) kept_scale<__half>(s, base, to, v, f);
+        else kept_scale<float>(s, base, to, v, f);
     } else {
-        table_scale<true>(tab, c, f);
+        table_scale(tab, c, f);
     }
 }
 
